@@ -18,8 +18,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libfourtune.so")
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "gemm_mlp.hip", "lora.hip", "act.hip",
-           "scratch.hip"]
+SOURCES = ["api.cpp", "api_block.cpp", "quantize.hip", "gemm.hip", "gemm_mlp.hip", "lora.hip",
+           "act.hip", "scratch.hip", "norm.hip", "norm_bwd.hip", "rope.hip", "attn.hip",
+           "attn_bwd.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -1,16 +1,10 @@
 // libfourtune C ABI (include/fourtune.h): argument checks, workspace layout
 // and kernel dispatch.  Every check runs before the first launch, so a call
 // that fails has enqueued nothing.
-#include "../../include/fourtune.h"
-
-#include <hip/hip_runtime.h>
-
 #include <algorithm>
-#include <atomic>
 #include <cstring>
-#include <mutex>
-#include <vector>
 
+#include "api_common.hpp"
 #include "ft_kernels.h"
 
 namespace ft {
@@ -30,19 +24,15 @@ int cu_count() {
 
 }  // namespace ft
 
+namespace ft {
+namespace api {
+
 namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-constexpr int64_t kMaxDim = int64_t(1) << 30;
-// Kernels address tensors with 32-bit buffer offsets.
-constexpr int64_t kMaxBytes = (int64_t(1) << 31) - 1;
-
 // 1 = current device is gfx950, 0 = not, 0 also before the first query
 // (then the query runs; racing first calls both store the same answer).
 // Cached per device.
 std::atomic<int> g_arch_ok[64];
+}  // namespace
 
 ft_status device_check() {
   int dev = 0;
@@ -58,78 +48,27 @@ ft_status device_check() {
   return ok == 1 ? FT_OK : FT_EUNSUPPORTED;
 }
 
-ft_status launched(hipError_t e) { return e == hipSuccess ? FT_OK : FT_EDEVICE; }
-
-// ---- optional per-kernel timing (benchmarks): hipEvents around each launch
-// Kernel names are string literals (static storage), so the pointers handed
-// out by fourtune_timing_read stay valid for the life of the process.
-struct TimingState {
-  std::mutex mu;
-  std::atomic<bool> on{false};
-  std::vector<hipEvent_t> pool;
-  struct Pending { int slot; hipEvent_t a, b; };
-  std::vector<Pending> pending;
-  std::vector<const char*> names;
-  std::vector<double> total_ms;
-  std::vector<int64_t> counts;
-  int slot(const char* n) {
-    for (size_t i = 0; i < names.size(); ++i)
-      if (std::strcmp(names[i], n) == 0) return static_cast<int>(i);
-    names.push_back(n);
-    total_ms.push_back(0.0);
-    counts.push_back(0);
-    return static_cast<int>(names.size() - 1);
-  }
-  hipEvent_t take() {
-    if (pool.empty()) {
-      hipEvent_t e = nullptr;
-      if (hipEventCreate(&e) != hipSuccess) return nullptr;
-      return e;
-    }
-    hipEvent_t e = pool.back();
-    pool.pop_back();
-    return e;
-  }
-  void drain() {  // caller holds mu
-    for (auto& p : pending) {
-      float ms = 0.f;
-      if (hipEventSynchronize(p.b) == hipSuccess && hipEventElapsedTime(&ms, p.a, p.b) == hipSuccess) {
-        total_ms[p.slot] += ms;
-        counts[p.slot] += 1;
-      }
-      pool.push_back(p.a);
-      pool.push_back(p.b);
-    }
-    pending.clear();
-  }
-};
 TimingState g_tm;
-// Set by the entry point that allocates nothing while it runs: no timing
-// events are created for its launches (creating one allocates).
 thread_local bool t_no_timing = false;
 
-// Brackets one launch with events when timing is on.
-struct Timed {
-  hipEvent_t a = nullptr, b = nullptr;
-  int slot = -1;
-  hipStream_t st;
-  Timed(const char* name, hipStream_t s) : st(s) {
-    if (t_no_timing || !g_tm.on.load(std::memory_order_relaxed)) return;
-    std::lock_guard<std::mutex> lk(g_tm.mu);
-    slot = g_tm.slot(name);
-    a = g_tm.take();
-    b = g_tm.take();
-    if (a && b) hipEventRecord(a, st);
-  }
-  hipError_t done(hipError_t e) {
-    if (a && b) {
-      hipEventRecord(b, st);
-      std::lock_guard<std::mutex> lk(g_tm.mu);
-      g_tm.pending.push_back({slot, a, b});
-    }
-    return e;
-  }
-};
+int TimingState::slot(const char* n) {
+  for (size_t i = 0; i < names.size(); ++i)
+    if (std::strcmp(names[i], n) == 0) return static_cast<int>(i);
+  names.push_back(n);
+  total_ms.push_back(0.0);
+  counts.push_back(0);
+  return static_cast<int>(names.size() - 1);
+}
+
+}  // namespace api
+}  // namespace ft
+
+namespace {
+
+using namespace ft::api;
+
+// Kernels address tensors with 32-bit buffer offsets.
+constexpr int64_t kMaxBytes = (int64_t(1) << 31) - 1;
 
 // The backward's dgrad computes the adapter gradients on the CUs its tiles
 // leave free when at least this many are free.

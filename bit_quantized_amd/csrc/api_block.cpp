@@ -1,0 +1,438 @@
+// libfourtune C ABI (include/fourtune.h), around the linears: the gated
+// residual and modulated norm, the rotation, attention inside documents and
+// the adapters' optimizer step.  Argument checks and dispatch; every check
+// runs before the first launch.
+#include <cmath>
+#include <cstring>
+
+#include "api_common.hpp"
+#include "ft_kernels.h"
+
+namespace {
+
+using namespace ft::api;
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool bad16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p && !aligned16(p)) return true;
+  return false;
+}
+inline bool is_dtype(int d) { return d == FT_BF16 || d == FT_F32; }
+// A row stride of rows of at least n elements: whole 16-byte pieces of bf16.
+inline ft_status check_ld(int64_t ld, int64_t n) {
+  return ld < n || (ld & 7) ? FT_EALIGN : ld > kMaxDim ? FT_ESHAPE : FT_OK;
+}
+
+// ---------------------------------------------------------------- norm
+ft_status norm_shape(const ft_norm* d) {
+  if (!d) return FT_EINVAL;
+  if (d->M < 0 || d->M > kMaxDim || d->C < 8 || d->C > 16384 || (d->C & 7)) return FT_ESHAPE;
+  if (d->n_seg < 1 || d->n_seg > 65000) return FT_ESHAPE;
+  if (!d->seg && d->M % d->n_seg != 0) return FT_ESHAPE;
+  if (!is_dtype(d->stream_dtype)) return FT_EINVAL;
+  if (!aligned4(d->seg)) return FT_EALIGN;
+  return FT_OK;
+}
+ft_status norm_factors(const ft_norm* d, bool has_norm, bool has_y) {
+  if (has_norm && d->norm != FT_NORM_RMS && d->norm != FT_NORM_LAYER) return FT_EINVAL;
+  if (has_y && (d->post_norm < FT_NORM_NONE || d->post_norm > FT_NORM_LAYER)) return FT_EINVAL;
+  if (!(d->eps >= 0.0f) || !std::isfinite(d->eps) || !std::isfinite(d->alpha)) return FT_EINVAL;
+  if (has_norm && bad16({d->weight, d->scale, d->shift})) return FT_EALIGN;
+  if (has_y && bad16({d->post_weight, d->gate})) return FT_EALIGN;
+  if ((has_norm && (d->scale || d->shift)) || (has_y && d->gate))
+    return check_ld(d->ld_mod, d->C);
+  return FT_OK;
+}
+ft::NormArgs norm_args(const ft_norm* d, bool has_norm, bool has_y) {
+  ft::NormArgs a{};
+  a.M = d->M; a.C = d->C; a.ld_mod = d->ld_mod;
+  a.n_seg = d->n_seg; a.seg = d->seg;
+  a.rows_per_seg = static_cast<int>(d->M / d->n_seg);
+  a.norm = d->norm; a.post_norm = d->post_norm; a.f32 = d->stream_dtype == FT_F32;
+  a.eps = d->eps; a.alpha = d->alpha;
+  if (has_norm) { a.weight = d->weight; a.scale = d->scale; a.shift = d->shift; }
+  if (has_y) { a.post_weight = d->post_weight; a.gate = d->gate; }
+  return a;
+}
+
+// ---------------------------------------------------------------- rope
+ft_status rope_table(const ft_rope* rp) {
+  if (!rp) return FT_EINVAL;
+  if (rp->D < 8 || rp->D > FT_ROPE_MAX_DIM || (rp->D & 7)) return FT_ESHAPE;
+  if (rp->n_axes < 1 || rp->n_axes > FT_ROPE_MAX_AXES) return FT_ESHAPE;
+  if (rp->n_pairs < 1 || 2 * rp->n_pairs > rp->D) return FT_ESHAPE;
+  if (rp->layout != FT_ROPE_PAIRS && rp->layout != FT_ROPE_HALVES) return FT_EINVAL;
+  if (rp->layout == FT_ROPE_HALVES && (rp->n_pairs & 7)) return FT_ESHAPE;
+  for (int j = 0; j < rp->n_pairs; ++j)
+    if (rp->axis[j] < 0 || rp->axis[j] >= rp->n_axes) return FT_EINVAL;
+  return FT_OK;
+}
+ft_status rope_side(const ft_rope* rp, const ft_rope_side* s) {
+  if (!s) return FT_EINVAL;
+  if (s->heads < 0 || s->heads > 65536) return FT_ESHAPE;
+  if (s->heads == 0) return FT_OK;
+  if (!s->in || !s->out) return FT_EINVAL;
+  const int64_t n = static_cast<int64_t>(s->heads) * rp->D;
+  if (ft_status e = check_ld(s->ld_in, n); e != FT_OK) return e;
+  if (ft_status e = check_ld(s->ld_out, n); e != FT_OK) return e;
+  if (s->in == s->out && s->ld_in != s->ld_out) return FT_EINVAL;
+  return bad16({s->in, s->out, s->weight}) ? FT_EALIGN : FT_OK;
+}
+ft_status rope_check(const ft_rope* rp, int64_t M, const int32_t* pos, float eps,
+                     const ft_rope_side* q, const ft_rope_side* k) {
+  if (ft_status e = rope_table(rp); e != FT_OK) return e;
+  if (M < 0 || M > kMaxDim) return FT_ESHAPE;
+  if (!pos || !(eps >= 0.0f) || !std::isfinite(eps)) return FT_EINVAL;
+  if (ft_status e = rope_side(rp, q); e != FT_OK) return e;
+  if (ft_status e = rope_side(rp, k); e != FT_OK) return e;
+  return aligned4(pos) ? FT_OK : FT_EALIGN;
+}
+ft::RopeArgs rope_args(const ft_rope* rp, int64_t M, const int32_t* pos, float eps,
+                       const ft_rope_side* q, const ft_rope_side* k) {
+  static_assert(sizeof(ft::RopeTable) == sizeof(ft_rope), "the table is the ABI's struct");
+  ft::RopeArgs a{};
+  a.M = M; a.pos = pos; a.eps = eps;
+  std::memcpy(&a.t, rp, sizeof(a.t));
+  const ft_rope_side* s[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    a.side[i].heads = s[i]->heads;
+    a.side[i].in = s[i]->in; a.side[i].out = s[i]->out;
+    a.side[i].ld_in = s[i]->ld_in; a.side[i].ld_out = s[i]->ld_out;
+    a.side[i].weight = s[i]->weight;
+  }
+  return a;
+}
+
+// ---------------------------------------------------------------- attn
+ft_status attn_shape(const ft_attn* d) {
+  if (!d) return FT_EINVAL;
+  if (d->M < 0 || d->M > kMaxDim) return FT_ESHAPE;
+  if (d->D != 64 && d->D != 128) return FT_ESHAPE;
+  if (d->Hq < 1 || d->Hkv < 1 || d->Hq > 1024 || d->Hq % d->Hkv != 0) return FT_ESHAPE;
+  if (d->n_doc < 1 || d->n_doc > (1 << 20) || (!d->doc && d->n_doc != 1)) return FT_ESHAPE;
+  // tiles of at least 64 rows, times heads, are one grid
+  if ((d->M / 64 + d->n_doc + 2) * d->Hq > (int64_t(1) << 30)) return FT_ESHAPE;
+  return FT_OK;
+}
+// Rows reach at most 64 strides in 32-bit offsets.
+ft_status attn_ld(int64_t ld, int64_t n) {
+  if (ft_status e = check_ld(ld, n); e != FT_OK) return e;
+  return ld > (int64_t(1) << 22) ? FT_ESHAPE : FT_OK;
+}
+ft_status attn_check(const ft_attn* d) {
+  if (ft_status e = attn_shape(d); e != FT_OK) return e;
+  if (d->mask < FT_MASK_FULL || d->mask > FT_MASK_PREFIX) return FT_EINVAL;
+  if (d->mask == FT_MASK_PREFIX && !d->prefix) return FT_EINVAL;
+  if (!(d->scale > 0.0f) || !std::isfinite(d->scale)) return FT_EINVAL;
+  if (!(d->softcap >= 0.0f) || !std::isfinite(d->softcap)) return FT_EINVAL;
+  if (!aligned4(d->doc) || !aligned4(d->prefix)) return FT_EALIGN;
+  const int64_t nq = static_cast<int64_t>(d->Hq) * d->D, nk = static_cast<int64_t>(d->Hkv) * d->D;
+  if (ft_status e = attn_ld(d->ld_q, nq); e != FT_OK) return e;
+  if (ft_status e = attn_ld(d->ld_k, nk); e != FT_OK) return e;
+  if (ft_status e = attn_ld(d->ld_v, nk); e != FT_OK) return e;
+  return attn_ld(d->ld_o, nq);
+}
+ft::AttnArgs attn_args(const ft_attn* d, const uint16_t* q, const uint16_t* k, const uint16_t* v) {
+  ft::AttnArgs a{};
+  a.M = d->M; a.Hq = d->Hq; a.Hkv = d->Hkv; a.mask = d->mask;
+  a.scale = d->scale; a.softcap = d->softcap;
+  a.n_doc = d->n_doc; a.doc = d->doc; a.prefix = d->mask == FT_MASK_PREFIX ? d->prefix : nullptr;
+  a.q = q; a.k = k; a.v = v;
+  a.ld_q = d->ld_q; a.ld_k = d->ld_k; a.ld_v = d->ld_v; a.ld_o = d->ld_o;
+  return a;
+}
+
+// ---------------------------------------------------------------- adamw
+constexpr int64_t kArenaMax = (int64_t(1) << 32) - 128;
+inline int64_t up128(int64_t n) { return (n + 127) & ~int64_t(127); }
+struct AdamwSizes {
+  int64_t arena = 0, chunks = 0;
+  size_t bytes(int32_t n) const {
+    return align_up(static_cast<size_t>(n) * sizeof(ft::AdamwEntry)) +
+           static_cast<size_t>(chunks) * sizeof(ft::AdamwChunk);
+  }
+};
+bool adamw_sizes(const ft_adamw_tensor* t, int32_t n, AdamwSizes* s) {
+  if (!t || n < 1) return false;
+  for (int32_t i = 0; i < n; ++i) {
+    if (t[i].n < 0 || t[i].n > kArenaMax) return false;
+    s->arena += up128(t[i].n);
+    s->chunks += (t[i].n + ft::kAdamwChunk - 1) / ft::kAdamwChunk;
+    if (s->arena > kArenaMax) return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+ft_status fourtune_norm_fwd(const ft_norm* d, const void* x, const uint16_t* y, void* r,
+                            uint16_t* h, float* stats, void* stream) {
+  if (ft_status e = norm_shape(d); e != FT_OK) return e;
+  if (!x || (y && !r) || (!y && !r && !h)) return FT_EINVAL;
+  if (ft_status e = norm_factors(d, h != nullptr, y != nullptr); e != FT_OK) return e;
+  if (bad16({x, y, r, h, stats})) return FT_EALIGN;
+  if (d->M == 0) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  ft::NormArgs a = norm_args(d, h != nullptr, y != nullptr);
+  a.x = x; a.y = y; a.r = r; a.h = h; a.stats = stats;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("norm_fwd", st);
+  return launched(tm.done(ft::launch_norm_fwd(a, st)));
+}
+
+size_t fourtune_norm_workspace_bytes(const ft_norm* d) {
+  return norm_shape(d) == FT_OK ? align_up(ft::norm_part_bytes(d->M, d->C, d->n_seg)) : 0;
+}
+
+ft_status fourtune_norm_bwd(const ft_norm* d, const uint16_t* dh, const void* dr, const void* r,
+                            const uint16_t* y, const float* stats, void* dx, uint16_t* dy,
+                            void* dscale, void* dshift, void* dgate, int64_t ld_dmod,
+                            void* dweight, void* dpost_weight, ft_dtype grad_dtype,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  if (ft_status e = norm_shape(d); e != FT_OK) return e;
+  if (!dx || (!dh && !dr) || (!dh && !y)) return FT_EINVAL;
+  if (y && !dy) return FT_EINVAL;
+  if (dh && !r) return FT_EINVAL;
+  if (ft_status e = norm_factors(d, dh != nullptr, y != nullptr); e != FT_OK) return e;
+  if ((dh || (y && d->post_norm != FT_NORM_NONE)) && !stats) return FT_EINVAL;
+  if ((dscale || dshift || dweight) && !dh) return FT_EINVAL;
+  if ((dgate || dpost_weight) && !y) return FT_EINVAL;
+  if (!is_dtype(grad_dtype)) return FT_EINVAL;
+  if (bad16({dh, dr, r, y, stats, dx, dy, dscale, dshift, dgate, dweight, dpost_weight, workspace}))
+    return FT_EALIGN;
+  if (dscale || dshift || dgate)
+    if (ft_status e = check_ld(ld_dmod, d->C); e != FT_OK) return e;
+  const bool sums = dscale || dshift || dgate || dweight || dpost_weight;
+  if (sums) {
+    if (ws_bytes < fourtune_norm_workspace_bytes(d)) return FT_EWORKSPACE;
+    if (!workspace) return FT_EINVAL;
+  }
+  if (d->M == 0 && !sums) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  ft::NormArgs a = norm_args(d, dh != nullptr, y != nullptr);
+  a.ld_dmod = ld_dmod;
+  a.dh = dh; a.dr = dr; a.x = r; a.y = y; a.stats = const_cast<float*>(stats);
+  a.dx = dx; a.dy = dy;
+  a.dscale = dscale; a.dshift = dshift; a.dgate = dgate;
+  a.dweight = dweight; a.dpost_weight = dpost_weight;
+  a.grad_f32 = grad_dtype == FT_F32;
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("norm_bwd", st);
+  return launched(tm.done(ft::launch_norm_bwd(a, st)));
+}
+
+ft_status fourtune_rope_init(ft_rope* rp, int32_t D, int32_t n_axes, const int32_t* axis_dims,
+                             double theta, int32_t layout, int32_t ladder) {
+  if (!rp || !axis_dims || !(theta > 0.0) || !std::isfinite(theta)) return FT_EINVAL;
+  if (layout != FT_ROPE_PAIRS && layout != FT_ROPE_HALVES) return FT_EINVAL;
+  if (ladder != FT_ROPE_AXIS && ladder != FT_ROPE_SHARED) return FT_EINVAL;
+  if (D < 8 || D > FT_ROPE_MAX_DIM || (D & 7)) return FT_ESHAPE;
+  if (n_axes < 1 || n_axes > FT_ROPE_MAX_AXES) return FT_ESHAPE;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n_axes; ++i) {
+    if (axis_dims[i] < 2 || axis_dims[i] > D || (axis_dims[i] & 1)) return FT_ESHAPE;
+    total += axis_dims[i];
+  }
+  if (total > D || (layout == FT_ROPE_HALVES && (total & 15))) return FT_ESHAPE;
+  std::memset(rp, 0, sizeof(*rp));
+  rp->D = D; rp->n_axes = n_axes; rp->layout = layout;
+  rp->n_pairs = static_cast<int32_t>(total / 2);
+  int32_t j = 0;
+  for (int32_t i = 0; i < n_axes; ++i)
+    for (int32_t k = 0; k < axis_dims[i] / 2; ++k, ++j) {
+      const double power = ladder == FT_ROPE_SHARED ? static_cast<double>(j) / rp->n_pairs
+                                                    : 2.0 * k / axis_dims[i];
+      const double turns = std::pow(theta, -power) / 6.283185307179586476925286766559;
+      rp->axis[j] = i;
+      rp->turn_hi[j] = static_cast<float>(turns);
+      rp->turn_lo[j] = static_cast<float>(turns - static_cast<double>(rp->turn_hi[j]));
+    }
+  return FT_OK;
+}
+
+ft_status fourtune_rope_fwd(const ft_rope* rp, int64_t M, const int32_t* positions, float eps,
+                            const ft_rope_side* q, const ft_rope_side* k, void* stream) {
+  if (ft_status e = rope_check(rp, M, positions, eps, q, k); e != FT_OK) return e;
+  if (M == 0 || q->heads + k->heads == 0) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  const ft::RopeArgs a = rope_args(rp, M, positions, eps, q, k);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("rope_fwd", st);
+  return launched(tm.done(ft::launch_rope(a, false, st)));
+}
+
+size_t fourtune_rope_workspace_bytes(const ft_rope* rp, int64_t M) {
+  if (rope_table(rp) != FT_OK || M < 0 || M > kMaxDim) return 0;
+  return align_up(ft::rope_part_bytes(M, rp->D) + 1);
+}
+
+ft_status fourtune_rope_bwd(const ft_rope* rp, int64_t M, const int32_t* positions, float eps,
+                            const ft_rope_side* q, const ft_rope_side* k, const uint16_t* q_x,
+                            int64_t ld_qx, const uint16_t* k_x, int64_t ld_kx, void* dq_weight,
+                            void* dk_weight, ft_dtype grad_dtype, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  if (ft_status e = rope_check(rp, M, positions, eps, q, k); e != FT_OK) return e;
+  if (!is_dtype(grad_dtype)) return FT_EINVAL;
+  const ft_rope_side* s[2] = {q, k};
+  const uint16_t* xs[2] = {q_x, k_x};
+  const int64_t lds[2] = {ld_qx, ld_kx};
+  void* dws[2] = {dq_weight, dk_weight};
+  ft::RopeArgs a = rope_args(rp, M, positions, eps, q, k);
+  for (int i = 0; i < 2; ++i) {
+    const bool norm = s[i]->heads > 0 && s[i]->weight;
+    if (dws[i] && !norm) return FT_EINVAL;
+    if (!norm) continue;
+    if (!xs[i]) return FT_EINVAL;
+    if (ft_status e = check_ld(lds[i], static_cast<int64_t>(s[i]->heads) * rp->D); e != FT_OK) return e;
+    a.side[i].x = xs[i]; a.side[i].ld_x = lds[i]; a.side[i].dweight = dws[i];
+  }
+  if (bad16({q_x, k_x, dq_weight, dk_weight, workspace})) return FT_EALIGN;
+  if (dq_weight || dk_weight) {
+    if (ws_bytes < fourtune_rope_workspace_bytes(rp, M)) return FT_EWORKSPACE;
+    if (!workspace) return FT_EINVAL;
+    a.part = static_cast<float*>(workspace);
+  }
+  if (q->heads + k->heads == 0 || (M == 0 && !a.part)) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  a.grad_f32 = grad_dtype == FT_F32;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("rope_bwd", st);
+  return launched(tm.done(ft::launch_rope(a, true, st)));
+}
+
+ft_status fourtune_attn_fwd(const ft_attn* d, const uint16_t* q, const uint16_t* k,
+                            const uint16_t* v, uint16_t* o, float* lse, void* stream) {
+  if (ft_status e = attn_check(d); e != FT_OK) return e;
+  if (!q || !k || !v || !o) return FT_EINVAL;
+  if (bad16({q, k, v, o, lse})) return FT_EALIGN;
+  if (d->M == 0) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  ft::AttnArgs a = attn_args(d, q, k, v);
+  a.o = o; a.lse = lse;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("attn_fwd", st);
+  return launched(tm.done(ft::launch_attn_fwd(a, d->D, st)));
+}
+
+size_t fourtune_attn_workspace_bytes(const ft_attn* d) {
+  if (attn_shape(d) != FT_OK) return 0;
+  return align_up(static_cast<size_t>(d->M) * d->Hq * sizeof(float) + 1);
+}
+
+ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do,
+                            const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                            const uint16_t* o, const float* lse, uint16_t* dq, int64_t ld_dq,
+                            uint16_t* dk, int64_t ld_dk, uint16_t* dv, int64_t ld_dv,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  if (ft_status e = attn_check(d); e != FT_OK) return e;
+  if (!d_o || !q || !k || !v || !o || !lse || !dq || !dk || !dv) return FT_EINVAL;
+  const int64_t nq = static_cast<int64_t>(d->Hq) * d->D, nk = static_cast<int64_t>(d->Hkv) * d->D;
+  if (ft_status e = attn_ld(ld_do, nq); e != FT_OK) return e;
+  if (ft_status e = attn_ld(ld_dq, nq); e != FT_OK) return e;
+  if (ft_status e = attn_ld(ld_dk, nk); e != FT_OK) return e;
+  if (ft_status e = attn_ld(ld_dv, nk); e != FT_OK) return e;
+  if (bad16({d_o, q, k, v, o, lse, dq, dk, dv, workspace})) return FT_EALIGN;
+  if (ws_bytes < fourtune_attn_workspace_bytes(d)) return FT_EWORKSPACE;
+  if (!workspace) return FT_EINVAL;
+  if (d->M == 0) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  ft::AttnArgs a = attn_args(d, q, k, v);
+  a.o_in = o; a.lse = const_cast<float*>(lse);
+  a.d_o = d_o; a.ld_do = ld_do;
+  a.dq = dq; a.dk = dk; a.dv = dv;
+  a.ld_dq = ld_dq; a.ld_dk = ld_dk; a.ld_dv = ld_dv;
+  a.delta = static_cast<float*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("attn_bwd", st);
+  return launched(tm.done(ft::launch_attn_bwd(a, d->D, st)));
+}
+
+size_t fourtune_adamw_plan_bytes(const ft_adamw_tensor* tensors, int32_t n_tensors,
+                                 int64_t* arena) {
+  AdamwSizes s;
+  if (!adamw_sizes(tensors, n_tensors, &s)) return 0;
+  if (arena) *arena = s.arena;
+  return s.bytes(n_tensors);
+}
+
+ft_status fourtune_adamw_plan(const ft_adamw_tensor* tensors, int32_t n_tensors,
+                              int32_t param_dtype, int32_t grad_dtype, int32_t state,
+                              ft_adamw* d, void* host_table, size_t table_bytes) {
+  if (!tensors || !d || !host_table || n_tensors < 1) return FT_EINVAL;
+  if (!is_dtype(param_dtype) || !is_dtype(grad_dtype)) return FT_EINVAL;
+  if (state != FT_STATE_F32 && state != FT_STATE_Q8) return FT_EINVAL;
+  AdamwSizes s;
+  if (!adamw_sizes(tensors, n_tensors, &s)) return FT_ESHAPE;
+  if (table_bytes < s.bytes(n_tensors)) return FT_EWORKSPACE;
+  const bool master = tensors[0].master != nullptr;
+  if (master && param_dtype != FT_BF16) return FT_EINVAL;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const ft_adamw_tensor& t = tensors[i];
+    if ((t.master != nullptr) != master) return FT_EINVAL;
+    if (t.n > 0 && (!t.p || !t.g)) return FT_EINVAL;
+    if (bad16({t.p, t.g, t.master})) return FT_EALIGN;
+  }
+  auto* entries = static_cast<ft::AdamwEntry*>(host_table);
+  auto* chunks = reinterpret_cast<ft::AdamwChunk*>(
+      static_cast<uint8_t*>(host_table) +
+      align_up(static_cast<size_t>(n_tensors) * sizeof(ft::AdamwEntry)));
+  int64_t at = 0, c = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const ft_adamw_tensor& t = tensors[i];
+    entries[i] = ft::AdamwEntry{t.p, t.g, t.master, t.n, at};
+    at += up128(t.n);
+    for (int64_t j = 0; j * ft::kAdamwChunk < t.n; ++j)
+      chunks[c++] = ft::AdamwChunk{static_cast<uint32_t>(i), static_cast<uint32_t>(j)};
+  }
+  std::memset(d, 0, sizeof(*d));
+  d->n_tensors = n_tensors;
+  d->param_dtype = param_dtype; d->grad_dtype = grad_dtype; d->state = state;
+  d->has_master = master;
+  d->arena = s.arena; d->n_chunks = s.chunks;
+  return FT_OK;
+}
+
+ft_status fourtune_adamw_step(const ft_adamw* d, int64_t t, double lr, double beta1, double beta2,
+                              double eps, double weight_decay, uint32_t seed,
+                              const float* grad_scale, void* stream) {
+  if (!d || d->n_tensors < 1 || d->n_chunks < 0) return FT_EINVAL;
+  if (!is_dtype(d->param_dtype) || !is_dtype(d->grad_dtype)) return FT_EINVAL;
+  if (d->state != FT_STATE_F32 && d->state != FT_STATE_Q8) return FT_EINVAL;
+  if (d->n_chunks > 0 && (!d->table || !d->m || !d->v)) return FT_EINVAL;
+  const bool q8 = d->state == FT_STATE_Q8;
+  if (q8 && d->n_chunks > 0 && (!d->m_scale || !d->v_scale)) return FT_EINVAL;
+  if (t < 1 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return FT_EINVAL;
+  if (!std::isfinite(lr) || !std::isfinite(weight_decay) || !(eps > 0.0) || !std::isfinite(eps))
+    return FT_EINVAL;
+  if (bad16({d->table, d->m, d->v, d->m_scale, d->v_scale}) || !aligned4(grad_scale)) return FT_EALIGN;
+  if (d->n_chunks == 0) return FT_OK;
+  if (ft_status e = device_check(); e != FT_OK) return e;
+  ft::AdamwArgs a{};
+  a.entries = static_cast<const ft::AdamwEntry*>(d->table);
+  a.chunks = reinterpret_cast<const ft::AdamwChunk*>(
+      static_cast<const uint8_t*>(d->table) +
+      align_up(static_cast<size_t>(d->n_tensors) * sizeof(ft::AdamwEntry)));
+  a.n_chunks = d->n_chunks;
+  a.m = d->m; a.v = d->v; a.m_scale = d->m_scale; a.v_scale = d->v_scale;
+  a.grad_scale = grad_scale;
+  const double td = static_cast<double>(t);
+  a.b1 = static_cast<float>(beta1); a.b1c = static_cast<float>(1.0 - beta1);
+  a.b2 = static_cast<float>(beta2); a.b2c = static_cast<float>(1.0 - beta2);
+  a.eps = static_cast<float>(eps);
+  a.decay = static_cast<float>(1.0 - lr * weight_decay);
+  a.rate = static_cast<float>(lr / (1.0 - std::pow(beta1, td)));
+  a.lift = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, td)));
+  a.key = seed * 0x9E3779B1u + static_cast<uint32_t>(t) * 0x510E527Fu;
+  a.p_kind = d->param_dtype == FT_F32 ? 0 : d->has_master ? 2 : 1;
+  a.g_f32 = d->grad_dtype == FT_F32;
+  a.q8 = q8;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Timed tm("adamw", st);
+  return launched(tm.done(ft::launch_adamw(a, st)));
+}
+
+}  // extern "C"

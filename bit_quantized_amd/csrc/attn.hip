@@ -1,0 +1,183 @@
+// Attention inside packed documents, forward:
+//   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i . k_j (capped by a tanh)
+// in one pass over the keys with the running maximum and sum of each query.
+//
+// A workgroup of four waves takes 128 queries of one document and head, a
+// wave 32 of them; key and value tiles of 64 rows go through LDS, the next
+// tile's loads in flight while one is worked on.  The products run as
+// 32x32x16 bf16 matrix instructions on the transposed problem: S^T = K Q^T
+// leaves a query's scores in two lanes (32 apart), so the softmax needs one
+// exchange per tile and its statistics are one value per lane; and the
+// accumulator's rows are, in order, the reduction slots of O^T = V^T P^T, if
+// V's columns are read with the same order of rows.  So P never leaves its
+// registers.  P is rounded to bf16 for that product (relative 2^-9, as the
+// output is); scores, statistics and the output accumulate in fp32.
+#include "attn_dev.hpp"
+
+namespace ft {
+
+using namespace attn_dev;
+
+namespace {
+
+constexpr int BM = 128, BN = 64;
+
+template <int D, bool CAP>
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
+  constexpr int KS = D / 16, DB = D / 32;
+  constexpr int TB = BN * D * 2;         // bytes of a tile
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TB];   // [buffer][K, V]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, half = lane >> 5;
+  const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int head = static_cast<int>(id / tiles);
+  DocTile dt;
+  if (!find_tile<BM>(a, static_cast<int>(id % tiles), dt)) return;
+  const int kvh = head / (a.Hq / a.Hkv);
+  const int qi = dt.row0 + wave * 32 + l32;              // this lane's query
+  const bool live = qi < dt.hi;
+  uint16_t* orow = a.o + static_cast<int64_t>(qi) * a.ld_o + head * D;
+  if (!dt.keys) {
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) reinterpret_cast<u32x4*>(orow)[2 * i + half] = u32x4{0, 0, 0, 0};
+      if (a.lse && half == 0) a.lse[head * a.M + qi] = kNegInf;
+    }
+    return;
+  }
+  // the tiles that some query of the workgroup sees
+  const int len = dt.hi - dt.lo;
+  const int q0 = dt.row0 - dt.lo;                        // in the document
+  const int seen = a.mask == 0 ? len : max(q0 + dt.rows, dt.prefix);
+  const int nt = (seen + BN - 1) / BN;
+  const uint16_t* kp = a.k + static_cast<int64_t>(dt.lo) * a.ld_k + kvh * D;
+  const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
+  auto fetch = [&](int t) {
+    uint8_t* buf = lds + (t & 1) * 2 * TB;
+    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane);
+    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane);
+  };
+  fetch(0);
+  u32x4 q[KS];
+  {
+    const uint16_t* qrow = a.q + static_cast<int64_t>(qi) * a.ld_q + head * D;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      q[ks] = u32x4{0, 0, 0, 0};
+      if (live) q[ks] = reinterpret_cast<const u32x4*>(qrow)[2 * ks + half];
+    }
+  }
+  uint32_t koff[KS], voff[DB][2];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) koff[ks] = row_off<D>(l32, half, ks);
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) voff[db][i] = col_off<D>(lane, db, i);
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) o[db] = zero16();
+  float m = kNegInf, l = 0.0f;
+  // scores in units of log 2: score * c1, or c2 tanh(score * c1)
+  const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
+  const float c2 = a.softcap * kLog2e;
+  const int wq0 = q0 + wave * 32;                        // the wave's first query
+  staged_barrier();
+  for (int t = 0; t < nt; ++t) {
+    if (t + 1 < nt) fetch(t + 1);
+    const uint8_t* kt = lds + (t & 1) * 2 * TB;
+    const uint8_t* vt = kt + TB;
+    f32x16 s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[kb] = zero16();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        s[kb] = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + koff[ks]), q[ks], s[kb]);
+    }
+    if constexpr (CAP) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[kb][r] = c2 * tanh_f32(s[kb][r] * c1);
+    }
+    const int last = t * BN + BN - 1;
+    if (last >= len || (a.mask != 0 && last > wq0 && last >= dt.prefix)) {
+      // keys from `end` on are hidden from this lane's query
+      const int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (t * BN + kb * 32 + acc_row(r, half) >= end) s[kb][r] = kNegInf;
+    }
+    float mt = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[kb][r]);
+    mt = halves_max(mt);
+    if constexpr (!CAP) mt *= c1;
+    // The statistics follow the maximum only when some query's rose by more
+    // than 2^8: until then p stays below 256, and the output needs no
+    // rescaling (its relative precision is the same).
+    if (__any(mt > m + 8.0f)) {
+      const float mn = fmaxf(m, mt);
+      const float f = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[db][r] *= f;
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[kb][r] = __builtin_amdgcn_exp2f(CAP ? s[kb][r] - m : __builtin_fmaf(s[kb][r], c1, -m));
+        sum += s[kb][r];
+      }
+      l += sum;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 p = pack8(s[kb], 8 * h);
+        const uint8_t* vk = vt + (kb * 32 + h * 16) * 2 * D;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+          o[db] = mfma_bf16_32x32x16(col_read(vk, voff[db][0], voff[db][1]), p, o[db]);
+      }
+    }
+    staged_barrier();
+  }
+  l = halves_sum(l);
+  const float inv = 1.0f / l;
+  if (live) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x2 w = {cvt_pk_bf16(o[db][4 * i] * inv, o[db][4 * i + 1] * inv),
+                         cvt_pk_bf16(o[db][4 * i + 2] * inv, o[db][4 * i + 3] * inv)};
+        *reinterpret_cast<u32x2*>(orow + db * 32 + 8 * i + 4 * half) = w;
+      }
+    if (a.lse && half == 0)
+      a.lse[head * a.M + qi] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<BM>(a));
+  const dim3 grid(tiles * static_cast<uint32_t>(a.Hq));
+#define FT_AF(DD, C) hipLaunchKernelGGL((k_attn_fwd<DD, C>), grid, dim3(256), 0, st, a, tiles)
+  if (D == 128) { if (a.softcap > 0) FT_AF(128, true); else FT_AF(128, false); }
+  else { if (a.softcap > 0) FT_AF(64, true); else FT_AF(64, false); }
+#undef FT_AF
+  return hipGetLastError();
+}
+
+}  // namespace ft

@@ -1,0 +1,184 @@
+// Shared by the attention kernels (attn.hip, attn_bwd.hip): which rows a
+// workgroup's tile has, the staging of 64-row tiles in LDS and the operand
+// reads from them.
+#pragma once
+
+#include "ft_device.hpp"
+#include "ft_kernels.h"
+
+namespace ft {
+namespace attn_dev {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNegInf = -__builtin_inff();
+
+// The rows of one tile: [row0, row0 + rows) of the document [lo, hi), whose
+// queries see keys lo .. (mask); keys = false: rows of no document.
+struct DocTile {
+  int row0, rows, lo, hi, prefix;
+  bool keys;
+};
+
+// Tile t of the rows cut into tiles of BM that do not cross documents.  The
+// rows before the first document and after the last count as two more
+// documents without keys, so every row is in exactly one tile.  Offsets are
+// clamped to [0, M]: whatever they hold, no row outside is touched.  The
+// lanes look at 64 documents at a time.  At most M / BM + n_doc + 2 tiles
+// exist; false for the launched ones past them.
+__device__ __forceinline__ int doc_bound(const AttnArgs& a, int i) {
+  if (i <= 0) return 0;
+  if (i > a.n_doc + 1) return static_cast<int>(a.M);
+  const int v = a.doc[i - 1];
+  return v < 0 ? 0 : v > a.M ? static_cast<int>(a.M) : v;
+}
+template <int BM>
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int t, DocTile& o) {
+  if (!a.doc) {
+    o.lo = 0;
+    o.hi = static_cast<int>(a.M);
+    o.row0 = t * BM;
+    o.keys = true;
+    o.prefix = a.mask == 2 ? a.prefix[0] : 0;
+    if (o.row0 >= o.hi) return false;
+  } else {
+    const int lane = threadIdx.x & 63;
+    const int nb = a.n_doc + 2;
+    int base = 0;
+    for (int d0 = 0;; d0 += 64) {
+      if (d0 >= nb) return false;
+      const int d = d0 + lane;
+      int lo = 0, hi = 0;
+      if (d < nb) {
+        lo = doc_bound(a, d);
+        hi = doc_bound(a, d + 1);
+      }
+      const int len = hi > lo ? hi - lo : 0;
+      const int n = (len + BM - 1) / BM;
+      int scan = n;
+#pragma unroll
+      for (int k = 1; k < 64; k *= 2) {
+        const int up = __shfl_up(scan, k);
+        if (lane >= k) scan += up;
+      }
+      const uint64_t past = __ballot(base + scan > t);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        o.lo = __builtin_amdgcn_readlane(lo, l);
+        o.hi = __builtin_amdgcn_readlane(hi, l);
+        o.row0 = o.lo + (t - (base + __builtin_amdgcn_readlane(scan, l) -
+                              __builtin_amdgcn_readlane(n, l))) * BM;
+        const int doc = d0 + l - 1;
+        o.keys = doc >= 0 && doc < a.n_doc;
+        o.prefix = a.mask == 2 && o.keys ? a.prefix[doc] : 0;
+        break;
+      }
+      base += __builtin_amdgcn_readlane(scan, 63);
+    }
+  }
+  o.rows = min(BM, o.hi - o.row0);
+  o.prefix = max(0, min(o.prefix, o.hi - o.lo));
+  return true;
+}
+template <int BM>
+inline int64_t tiles_of(const AttnArgs& a) {
+  return a.doc ? a.M / BM + a.n_doc + 2 : (a.M + BM - 1) / BM;
+}
+
+// A tile of rows in LDS: 2 D bytes a row, its 16-byte chunks permuted by
+// chunk ^ swz(row), so that both ways of reading it are free of bank
+// conflicts: 16 rows of one chunk (ds_read_b128 of a row operand), and 4
+// consecutive rows of 64 bytes (ds_read_b64_tr_b16 of a column operand).
+template <int D>
+__device__ __forceinline__ uint32_t swz(uint32_t row) {
+  return D == 128 ? ((row & 3u) << 2) | ((row >> 2) & 3u) : ((row & 2u) << 1) | ((row >> 2) & 3u);
+}
+
+// The LDS destination goes in as an opaque address, so that the compiler
+// does not wait for all loads in flight before the next LDS read; the
+// kernels wait themselves (vmcnt, then a barrier) before a tile is read.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
+  uint32_t l = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((FT_LDS uint8_t*)(lds)));
+  asm volatile("" : "+s"(l));
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (FT_LDS void*)(static_cast<uintptr_t>(l)), 16,
+                                           (int)off, 0, 0, 0);
+}
+// Start the loads of ROWS rows of D bf16 (the first at p, ld elements apart)
+// into `tile`, by NW waves; rows from `have` on become zeros.
+template <int D, int ROWS, int NW>
+__device__ __forceinline__ void stage(const uint16_t* p, int64_t ld, int have, uint8_t* tile,
+                                      int wave, int lane) {
+  constexpr int CH = D / 8;                    // chunks of a row
+  constexpr int RI = 64 / CH;                  // rows of one instruction
+  constexpr int N = ROWS / RI / NW;            // instructions of a wave
+  static_assert(N * RI * NW == ROWS, "the waves share the tile evenly");
+  const __amdgpu_buffer_rsrc_t r = make_rsrc(p, 0x7FFFFFFFu);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int first = (wave * N + i) * RI;
+    const int row = first + lane / CH;
+    const uint32_t c = (lane % CH) ^ swz<D>(row);
+    const uint32_t off = static_cast<uint32_t>(row) * static_cast<uint32_t>(ld) * 2u + c * 16u;
+    dma16(r, tile + first * (2 * D), row < have ? off : BUF_OOB);
+  }
+}
+__device__ __forceinline__ void staged_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Byte offset in a tile of the row operand of step ks (16 values of D): lane
+// l has values 16 ks + 8 (l / 32) .. +7 of row l % 32.
+template <int D>
+__device__ __forceinline__ uint32_t row_off(int l32, int half, int ks) {
+  return l32 * (2 * D) + (((2 * ks + half) ^ swz<D>(l32)) << 4);
+}
+// Byte offset of half i of the column operand of the first 16 rows: lane l
+// gets, through the transposing read, rows 4 (l / 32) + 8 i .. +3 of column
+// 32 db + l % 32; the two halves give the eight rows that the accumulator
+// of a 32x32 product leaves in a lane for its first 16 rows.
+template <int D>
+__device__ __forceinline__ uint32_t col_off(int lane, int db, int i) {
+  const uint32_t row = ((lane & 15) >> 2) + 4 * (lane >> 5) + 8 * i;
+  const uint32_t c = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  return row * (2 * D) + ((c ^ swz<D>(row)) << 4) + (lane & 1) * 8;
+}
+__device__ __forceinline__ u32x4 col_read(const uint8_t* tile, uint32_t off0, uint32_t off1) {
+  const u32x2 a = lds_read_tr16(tile + off0), b = lds_read_tr16(tile + off1);
+  return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// Reduce a value over a lane and the one 32 away.
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// tanh(x) through e = exp(2x): 1 - 2 / (e + 1), which saturates at both ends.
+__device__ __forceinline__ float tanh_f32(float x) {
+  const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
+  return __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
+}
+
+// Eight accumulator values as one operand of eight bf16.
+__device__ __forceinline__ u32x4 pack8(const f32x16& s, int first) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = cvt_pk_bf16(s[first + 2 * i], s[first + 2 * i + 1]);
+  return w;
+}
+
+// Where value r of a 32x32 accumulator lies: row 8 (r / 4) + 4 (lane / 32) + r % 4.
+__device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
+}  // namespace attn_dev
+}  // namespace ft

@@ -216,4 +216,107 @@ void* noalloc_scratch();
 hipError_t launch_act(int act, const uint16_t* h, const uint16_t* g, int64_t n, uint16_t* out,
                       hipStream_t st);
 
+// norm.hip, norm_bwd.hip: the gated residual and modulated norm (ft_norm of
+// the C ABI); kinds as FT_NORM_*.
+struct NormArgs {
+  int64_t M, C, ld_mod, ld_dmod;
+  int n_seg, rows_per_seg;        // rows_per_seg: used when seg is null
+  const int32_t* seg;
+  int norm, post_norm, f32;       // f32: the stream (x, r, dr, dx) is fp32
+  float eps, alpha;
+  const uint16_t *weight, *post_weight, *scale, *shift, *gate, *y;
+  const void* x;                  // forward: x; backward: r
+  void* r;
+  uint16_t* h;
+  float* stats;                   // [M, 4]: mean, rstd of r; mean, rstd of y
+  // backward
+  const uint16_t* dh;
+  const void* dr;
+  void* dx;
+  uint16_t* dy;
+  void *dscale, *dshift, *dgate, *dweight, *dpost_weight;
+  int grad_f32;
+  float* part;                    // null: none of the five is asked for
+  int rows_per_wg;                // set by launch_norm_bwd
+};
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st);
+size_t norm_part_bytes(int64_t M, int64_t C, int n_seg);
+
+// rope.hip: rotation of query and key heads (ft_rope of the C ABI).
+struct RopeTable {
+  int32_t D, n_axes, layout, n_pairs;
+  int32_t axis[128];
+  float turn_hi[128], turn_lo[128];
+};
+struct RopeSide {
+  int heads;
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t ld_in, ld_out;
+  const uint16_t* weight;         // null: no norm
+  const uint16_t* x;              // backward with a weight: the forward's input
+  int64_t ld_x;
+  void* dweight;
+};
+struct RopeArgs {
+  int64_t M;
+  const int32_t* pos;
+  float eps;
+  RopeSide side[2];
+  int grad_f32;
+  float* part;                    // backward: [workgroups][2][D] partial weight gradients, or null
+  RopeTable t;
+};
+hipError_t launch_rope(const RopeArgs& a, bool bwd, hipStream_t st);
+size_t rope_part_bytes(int64_t M, int D);
+
+// attn.hip, attn_bwd.hip: attention inside packed documents (ft_attn of the
+// C ABI).
+struct AttnArgs {
+  int64_t M;
+  int Hq, Hkv, mask;              // mask: FT_MASK_*
+  float scale, softcap;
+  int n_doc;
+  const int32_t* doc;             // null: one document of all rows
+  const int32_t* prefix;
+  const uint16_t *q, *k, *v;
+  int64_t ld_q, ld_k, ld_v, ld_o;
+  uint16_t* o;
+  float* lse;
+  // backward
+  const uint16_t *d_o, *o_in;
+  int64_t ld_do;
+  uint16_t *dq, *dk, *dv;
+  int64_t ld_dq, ld_dk, ld_dv;
+  float* delta;                   // [Hq, M]
+};
+hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st);
+hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st);
+
+// adamw.hip: one step over the tensors of a table (ft_adamw of the C ABI).
+struct AdamwEntry {               // one tensor
+  void* p;
+  const void* g;
+  float* master;
+  int64_t n, at;                  // elements; place in the state arenas
+};
+struct AdamwChunk {               // kAdamwChunk elements of one tensor
+  uint32_t tensor, chunk;
+};
+constexpr int kAdamwChunk = 2048;
+struct AdamwArgs {
+  const AdamwEntry* entries;
+  const AdamwChunk* chunks;
+  int64_t n_chunks;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  const float* grad_scale;
+  float b1, b1c, b2, b2c, eps, decay, rate, lift;
+  uint32_t key;
+  int p_kind;                     // 0 fp32, 1 bf16, 2 bf16 with a master
+  int g_f32, q8;
+};
+hipError_t launch_adamw(const AdamwArgs& a, hipStream_t st);
+
 }  // namespace ft

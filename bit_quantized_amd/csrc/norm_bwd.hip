@@ -1,0 +1,329 @@
+// The gated residual and modulated norm, backward.  With n = N(r), m = N_post(y)
+// and a = dh (1 + scale) weight:
+//   dx = dr + rstd (a - n mean(a n) [- mean(a) for LAYER])
+//   dy = rstd_y (e - m mean(e m) [- mean(e)]),   e = alpha dx gate post_weight
+//   (dy = e without a post norm)
+//   sums over the rows of a sample:  A1 = sum dh n,  A2 = sum dh,  A3 = sum dx m
+//   dscale = weight A1,  dshift = A2,  dgate = alpha post_weight A3
+//   sums over all samples:  dweight = sum (1 + scale_b) A1_b,
+//                           dpost_weight = alpha sum gate_b A3_b
+//
+// Memory bound: dh, dr, r, y are read once, dx and dy written once.  The
+// column sums A1..A3 stay in registers while a workgroup walks its rows, so
+// they cost one store of 3 C fp32 per workgroup and sample.  A workgroup
+// owns RC consecutive rows; the pairs (workgroup g, sample b) that meet form
+// a staircase, so g + b numbers them without gaps to search, and the second
+// kernel adds the slots of a sample in order (the same bits every time).
+#include <algorithm>
+
+#include "norm_dev.hpp"
+
+namespace ft {
+
+using namespace norm_dev;
+
+namespace {
+
+constexpr int kMaxWaves = 8;             // waves of a workgroup: 64 NV channel vectors each
+
+// Y: 0 no y, 1 y as it is, 2 y normalized; H: dh is given.  A workgroup has
+// a row at a time, each lane NV vectors of eight channels of it, and (where
+// the registers hold it, NV <= 2) the next row's loads in flight.
+template <int NV, int F32, int Y, int H>
+__global__ __launch_bounds__(kMaxWaves * 64) void k_norm_bwd(const NormArgs a) {
+  __shared__ float red[2][2][2][kMaxWaves];      // [row parity][which norm][sum][wave]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = static_cast<int>(blockDim.x >> 6);
+  const int nv = static_cast<int>(a.C >> 3);
+  const float inv_c = 1.0f / static_cast<float>(a.C);
+  const int lo = static_cast<int>(blockIdx.x) * a.rows_per_wg;
+  const int hi = min(lo + a.rows_per_wg, static_cast<int>(a.M));
+  int at[NV];
+  bool ok[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    at[i] = static_cast<int>(threadIdx.x + i * blockDim.x);
+    ok[i] = at[i] < nv;
+  }
+  int par = 0;
+  // two sums over the row at once
+  auto sum2 = [&](float& s, float& t, int k) {
+    s = lanes_sum<64>(s);
+    t = lanes_sum<64>(t);
+    if (waves > 1) {
+      if (lane == 0) {
+        red[par][k][0][wave] = s;
+        red[par][k][1][wave] = t;
+      }
+      __syncthreads();
+      const int w = lane & (kMaxWaves - 1);
+      s = lanes_sum<kMaxWaves>(w < waves ? red[par][k][0][w] : 0.0f);
+      t = lanes_sum<kMaxWaves>(w < waves ? red[par][k][1][w] : 0.0f);
+    }
+  };
+
+  int b = sample_of(a, lo);
+  for (int row0 = lo; row0 < hi; ++b) {
+    const int end = min(hi, sample_first(a, b + 1));
+    if (end <= row0) {
+      if (b >= a.n_seg) break;           // (offsets that do not ascend)
+      continue;
+    }
+    const int64_t mod8 = b * (a.ld_mod >> 3);
+    Raw8<0> sc[NV], w[NV], g[NV], pw[NV];
+    float A1[NV][8], A2[NV][8], A3[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c8 = ok[i] ? at[i] : 0;
+      if constexpr (H) {
+        sc[i] = factor(a.scale, mod8 + c8, 0u);
+        w[i] = factor(a.weight, c8, kOnes);
+      }
+      if constexpr (Y > 0) {
+        g[i] = factor(a.gate, mod8 + c8, kOnes);
+        pw[i] = factor(a.post_weight, c8, kOnes);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) A1[i][e] = A2[i][e] = A3[i][e] = 0.0f;
+    }
+    Raw8<F32> nr[NV], ndr[NV];
+    Raw8<0> ndh[NV], ny[NV];
+    f32x4 nst = {0.0f, 1.0f, 0.0f, 1.0f};
+    // the loads of a row (zeros past its end)
+    auto fetch = [&](int row) {
+      if (a.stats) nst = reinterpret_cast<const f32x4*>(a.stats)[row];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        nr[i].zero();
+        ndr[i].zero();
+        ndh[i].zero();
+        ny[i].zero();
+        if (ok[i]) {
+          const int64_t o = static_cast<int64_t>(row) * nv + at[i];
+          if constexpr (H) {
+            nr[i].load(a.x, o);
+            ndh[i].load(a.dh, o);
+          }
+          if (a.dr) ndr[i].load(a.dr, o);
+          if constexpr (Y > 0) ny[i].load(a.y, o);
+        }
+      }
+    };
+    constexpr bool AHEAD = NV <= 2;
+    if (AHEAD) fetch(row0);
+    for (int row = row0; row < end; ++row) {
+      if (!AHEAD) fetch(row);
+      Raw8<F32> cr[NV], cdr[NV];
+      Raw8<0> cdh[NV], cy[NV];
+      const f32x4 st = nst;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        cr[i] = nr[i];
+        cdr[i] = ndr[i];
+        cdh[i] = ndh[i];
+        cy[i] = ny[i];
+      }
+      if (AHEAD && row + 1 < end) fetch(row + 1);
+      float dx[NV][8];
+      if constexpr (H) {
+        float s = 0.0f, t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = cdh[i].get(e);
+            const float n = (cr[i].get(e) - st[0]) * st[1];
+            const float av = d * (1.0f + sc[i].get(e)) * w[i].get(e);
+            s += av;
+            t = __builtin_fmaf(av, n, t);
+            A1[i][e] = __builtin_fmaf(d, n, A1[i][e]);
+            A2[i][e] += d;
+            dx[i][e] = av;
+          }
+        sum2(s, t, 0);
+        const float ma = a.norm == 2 ? s * inv_c : 0.0f, mn = t * inv_c;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float n = (cr[i].get(e) - st[0]) * st[1];
+            dx[i][e] = __builtin_fmaf(st[1], dx[i][e] - ma - n * mn, cdr[i].get(e));
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dx[i][e] = cdr[i].get(e);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (ok[i]) {
+          Raw8<F32> o;
+          o.set(dx[i]);
+          o.store(a.dx, static_cast<int64_t>(row) * nv + at[i]);
+        }
+      if constexpr (Y > 0) {
+        float s = 0.0f, t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float m = Y == 2 ? (cy[i].get(e) - st[2]) * st[3] : cy[i].get(e);
+            const float d = ok[i] ? dx[i][e] : 0.0f;
+            A3[i][e] = __builtin_fmaf(d, m, A3[i][e]);
+            dx[i][e] = d * (a.alpha * g[i].get(e)) * pw[i].get(e);
+            if constexpr (Y == 2) {
+              s += dx[i][e];
+              t = __builtin_fmaf(dx[i][e], m, t);
+            }
+          }
+        if constexpr (Y == 2) {
+          sum2(s, t, 1);
+          const float ma = a.post_norm == 2 ? s * inv_c : 0.0f, mn = t * inv_c;
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float m = (cy[i].get(e) - st[2]) * st[3];
+              dx[i][e] = st[3] * (dx[i][e] - ma - m * mn);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (ok[i]) {
+            Raw8<0> o;
+            o.set(dx[i]);
+            o.store(a.dy, static_cast<int64_t>(row) * nv + at[i]);
+          }
+      }
+      par ^= 1;
+    }
+    // one store of the sample's sums
+    if (a.part) {
+      float* slot = a.part + static_cast<int64_t>(blockIdx.x + b) * 3 * a.C;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!ok[i]) continue;
+        Raw8<1> o;
+        if constexpr (H) {
+          o.set(A1[i]);
+          o.store(slot, at[i]);
+          o.set(A2[i]);
+          o.store(slot + a.C, at[i]);
+        }
+        if constexpr (Y > 0) {
+          o.set(A3[i]);
+          o.store(slot + 2 * a.C, at[i]);
+        }
+      }
+    }
+    row0 = end;
+  }
+}
+
+// The sums of each sample's slots and of all samples: one workgroup per 64
+// columns and sample (index n_seg: the weights' gradients), 16 threads a
+// column, whose partial sums are added in order.
+constexpr int kCols = 64, kWays = 16;
+__global__ __launch_bounds__(kCols* kWays) void k_norm_reduce(const NormArgs a) {
+  __shared__ float acc[kWays][kCols];
+  const int c = static_cast<int>(blockIdx.x) * kCols + (threadIdx.x & (kCols - 1));
+  const int way = threadIdx.x / kCols;
+  const int b = static_cast<int>(blockIdx.y);
+  const bool in = c < a.C;
+  const int kind = static_cast<int>(blockIdx.z);     // 0: A1, 1: A2, 2: A3
+  void* out = b < a.n_seg ? (kind == 0 ? a.dscale : kind == 1 ? a.dshift : a.dgate)
+                          : (kind == 0 ? a.dweight : kind == 2 ? a.dpost_weight : nullptr);
+  if (!out) return;
+  auto sum = [&](int s) {
+    float v = 0.0f;
+    const int r0 = sample_first(a, s), r1 = sample_first(a, s + 1);
+    if (r1 <= r0 || !in) return v;
+    const int g1 = (r1 - 1) / a.rows_per_wg;
+    const float* p = a.part + kind * a.C + c;
+    for (int g = r0 / a.rows_per_wg + way; g <= g1; g += kWays)
+      v += p[static_cast<int64_t>(g + s) * 3 * a.C];
+    return v;
+  };
+  auto ld = [&](const uint16_t* p, int64_t i, float none) { return p ? bf16_to_f32(p[i]) : none; };
+  float v = 0.0f;
+  if (b < a.n_seg) {
+    v = sum(b);
+  } else {
+    for (int s = 0; s < a.n_seg; ++s) {
+      const float f = !in ? 0.0f
+                      : kind == 0 ? 1.0f + ld(a.scale, s * a.ld_mod + c, 0.0f)
+                                  : a.alpha * ld(a.gate, s * a.ld_mod + c, 1.0f);
+      v = __builtin_fmaf(f, sum(s), v);
+    }
+  }
+  acc[way][threadIdx.x & (kCols - 1)] = v;
+  __syncthreads();
+  if (way != 0 || !in) return;
+  v = acc[0][threadIdx.x];
+#pragma unroll
+  for (int i = 1; i < kWays; ++i) v += acc[i][threadIdx.x];
+  int64_t o = c;
+  if (b < a.n_seg) {
+    o += b * a.ld_dmod;
+    if (kind == 0) v *= ld(a.weight, c, 1.0f);
+    if (kind == 2) v *= a.alpha * ld(a.post_weight, c, 1.0f);
+  }
+  if (a.grad_f32) static_cast<float*>(out)[o] = v;
+  else static_cast<uint16_t*>(out)[o] = static_cast<uint16_t>(cvt_pk_bf16(v, 0.0f));
+}
+
+// Vectors of a lane (1, 2 or 4) and waves of a workgroup.
+int vectors_of(int64_t C) { return C <= 4096 ? 1 : C <= 8192 ? 2 : 4; }
+int waves_of(int64_t C) {
+  const int64_t per = 512 * vectors_of(C);
+  return static_cast<int>((C + per - 1) / per);
+}
+// Rows of a workgroup: about 3072 waves on the chip, at least 8 rows each
+// so that the column sums' stores stay small beside the rows'.
+int rows_per_wg(int64_t M, int64_t C) {
+  const int64_t wgs = std::max(256, 3072 / waves_of(C));
+  return static_cast<int>(std::max<int64_t>(8, (M + wgs - 1) / wgs));
+}
+
+template <int NV>
+hipError_t go(const NormArgs& a, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>((a.M + a.rows_per_wg - 1) / a.rows_per_wg));
+  const dim3 block(static_cast<uint32_t>(64 * waves_of(a.C)));
+  const int y = !a.y ? 0 : a.post_norm == 0 ? 1 : 2;
+#define FT_NB(F, Y, H) hipLaunchKernelGGL((k_norm_bwd<NV, F, Y, H>), grid, block, 0, st, a)
+#define FT_NBF(F)                                                                    \
+  do {                                                                               \
+    if (a.dh) { if (y == 0) FT_NB(F, 0, 1); else if (y == 1) FT_NB(F, 1, 1); else FT_NB(F, 2, 1); } \
+    else { if (y == 1) FT_NB(F, 1, 0); else FT_NB(F, 2, 0); }                        \
+  } while (0)
+  if (a.f32) FT_NBF(1);
+  else FT_NBF(0);
+#undef FT_NBF
+#undef FT_NB
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t norm_part_bytes(int64_t M, int64_t C, int n_seg) {
+  const int64_t rc = rows_per_wg(M, C);
+  return static_cast<size_t>((M + rc - 1) / rc + n_seg) * 3 * C * sizeof(float);
+}
+
+hipError_t launch_norm_bwd(const NormArgs& in, hipStream_t st) {
+  NormArgs a = in;
+  a.rows_per_wg = rows_per_wg(a.M, a.C);
+  hipError_t e = hipSuccess;
+  if (a.M > 0) {
+    const int v = vectors_of(a.C);
+    e = v == 1 ? go<1>(a, st) : v == 2 ? go<2>(a, st) : go<4>(a, st);
+  }
+  if (e != hipSuccess || !a.part) return e;
+  const dim3 grid(static_cast<uint32_t>((a.C + kCols - 1) / kCols),
+                  static_cast<uint32_t>(a.n_seg + (a.dweight || a.dpost_weight ? 1 : 0)), 3);
+  hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kCols * kWays), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace ft

@@ -22,6 +22,12 @@ FT_NOALLOC_SCRATCH_BYTES = 64 << 20
 FT_ACT_NONE, FT_ACT_GELU_TANH = 0, 1
 FT_W4A4G4, FT_W4A16G4, FT_W4A4G16, FT_W4A16G16 = 0, 1, 2, 3
 FT_WBLOCK_TILE32, FT_WBLOCK_ROW32, FT_WBLOCK_TILE32_T = 0, 1, 2
+FT_NORM_NONE, FT_NORM_RMS, FT_NORM_LAYER = 0, 1, 2
+FT_ROPE_MAX_AXES, FT_ROPE_MAX_DIM = 4, 256
+FT_ROPE_PAIRS, FT_ROPE_HALVES = 0, 1
+FT_ROPE_AXIS, FT_ROPE_SHARED = 0, 1
+FT_MASK_FULL, FT_MASK_CAUSAL, FT_MASK_PREFIX = 0, 1, 2
+FT_STATE_F32, FT_STATE_Q8 = 0, 1
 PRECISION_NAMES = {"W4A4G4": FT_W4A4G4, "W4A16G4": FT_W4A16G4, "W4A4G16": FT_W4A4G16,
                    "W4A16G16": FT_W4A16G16}
 
@@ -29,6 +35,11 @@ EXPORTS = ("fourtune_quantize", "fourtune_dequantize", "fourtune_workspace_bytes
            "fourtune_linear_fwd_noalloc", "fourtune_linear_bwd", "fourtune_mlp_workspace_bytes",
            "fourtune_mlp_fwd", "fourtune_mlp_bwd_workspace_bytes", "fourtune_mlp_bwd",
            "fourtune_act_fwd", "fourtune_act_bwd",
+           "fourtune_norm_fwd", "fourtune_norm_workspace_bytes", "fourtune_norm_bwd",
+           "fourtune_rope_init", "fourtune_rope_fwd", "fourtune_rope_workspace_bytes",
+           "fourtune_rope_bwd", "fourtune_attn_fwd", "fourtune_attn_workspace_bytes",
+           "fourtune_attn_bwd", "fourtune_adamw_plan_bytes", "fourtune_adamw_plan",
+           "fourtune_adamw_step",
            "fourtune_status_string", "fourtune_timing_enable", "fourtune_timing_reset",
            "fourtune_timing_read")
 
@@ -48,6 +59,51 @@ class FtLinear(ctypes.Structure):
                 ("At", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("act_in", ctypes.c_int32), ("act_out", ctypes.c_int32),
                 ("precision", ctypes.c_int32), ("w_block", ctypes.c_int32)]
+
+
+class FtNorm(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("C", ctypes.c_int64), ("n_seg", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32), ("seg", ctypes.c_void_p),
+                ("norm", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("ld_mod", ctypes.c_int64)]
+
+
+class FtRope(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("n_pairs", ctypes.c_int32), ("axis", ctypes.c_int32 * (FT_ROPE_MAX_DIM // 2)),
+                ("turn_hi", ctypes.c_float * (FT_ROPE_MAX_DIM // 2)),
+                ("turn_lo", ctypes.c_float * (FT_ROPE_MAX_DIM // 2))]
+
+
+class FtRopeSide(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("inp", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("ld_in", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("weight", ctypes.c_void_p)]
+
+
+class FtAttn(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("mask", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("n_doc", ctypes.c_int32), ("doc", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p), ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64),
+                ("ld_v", ctypes.c_int64), ("ld_o", ctypes.c_int64)]
+
+
+class FtAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("n", ctypes.c_int64)]
+
+
+class FtAdamw(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+                ("has_master", ctypes.c_int32), ("arena", ctypes.c_int64),
+                ("n_chunks", ctypes.c_int64), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p)]
 
 
 _lib = None
@@ -90,6 +146,26 @@ def lib() -> ctypes.CDLL:
         L.fourtune_act_fwd.restype = st
         L.fourtune_act_bwd.argtypes = [st, vp, vp, i64, vp, vp]
         L.fourtune_act_bwd.restype = st
+        i32, f32, f64, sz, P = (ctypes.c_int32, ctypes.c_float, ctypes.c_double, ctypes.c_size_t,
+                                ctypes.POINTER)
+        for name, args, res in (
+                ("norm_fwd", [P(FtNorm)] + [vp] * 6, st),
+                ("norm_workspace_bytes", [P(FtNorm)], sz),
+                ("norm_bwd", [P(FtNorm)] + [vp] * 10 + [i64, vp, vp, st, vp, sz, vp], st),
+                ("rope_init", [P(FtRope), i32, i32, P(i32), f64, i32, i32], st),
+                ("rope_fwd", [P(FtRope), i64, vp, f32, P(FtRopeSide), P(FtRopeSide), vp], st),
+                ("rope_workspace_bytes", [P(FtRope), i64], sz),
+                ("rope_bwd", [P(FtRope), i64, vp, f32, P(FtRopeSide), P(FtRopeSide), vp, i64, vp,
+                              i64, vp, vp, st, vp, sz, vp], st),
+                ("attn_fwd", [P(FtAttn)] + [vp] * 6, st),
+                ("attn_workspace_bytes", [P(FtAttn)], sz),
+                ("attn_bwd", [P(FtAttn), vp, i64] + [vp] * 5 + [vp, i64] * 3 + [vp, sz, vp], st),
+                ("adamw_plan_bytes", [P(FtAdamwTensor), i32, P(i64)], sz),
+                ("adamw_plan", [P(FtAdamwTensor), i32, i32, i32, i32, P(FtAdamw), vp, sz], st),
+                ("adamw_step", [P(FtAdamw), i64, f64, f64, f64, f64, f64, ctypes.c_uint32, vp, vp],
+                 st)):
+            fn = getattr(L, "fourtune_" + name)
+            fn.argtypes, fn.restype = args, res
         L.fourtune_status_string.argtypes = [st]
         L.fourtune_status_string.restype = ctypes.c_char_p
         L.fourtune_timing_enable.argtypes = [st]
@@ -224,6 +300,96 @@ def fourtune_act_fwd(act, h, n, out, stream=None):
 def fourtune_act_bwd(act, h, g, n, out, stream=None):
     _check(lib().fourtune_act_bwd(int(act), _ptr(h), _ptr(g), int(n), _ptr(out), _stream(stream)),
            "fourtune_act_bwd")
+
+
+def fourtune_norm_fwd(d: FtNorm, x, y, r, h, stats, stream=None):
+    _check(lib().fourtune_norm_fwd(ctypes.byref(d), _ptr(x), _ptr(y), _ptr(r), _ptr(h), _ptr(stats),
+                                   _stream(stream)), "fourtune_norm_fwd")
+
+
+def fourtune_norm_workspace_bytes(d: FtNorm) -> int:
+    return int(lib().fourtune_norm_workspace_bytes(ctypes.byref(d)))
+
+
+def fourtune_norm_bwd(d: FtNorm, dh, dr, r, y, stats, dx, dy, dscale, dshift, dgate, ld_dmod,
+                      dweight, dpost_weight, grad_dtype, workspace, ws_bytes, stream=None):
+    _check(lib().fourtune_norm_bwd(ctypes.byref(d), _ptr(dh), _ptr(dr), _ptr(r), _ptr(y),
+                                   _ptr(stats), _ptr(dx), _ptr(dy), _ptr(dscale), _ptr(dshift),
+                                   _ptr(dgate), int(ld_dmod), _ptr(dweight), _ptr(dpost_weight),
+                                   int(grad_dtype), _ptr(workspace), int(ws_bytes),
+                                   _stream(stream)), "fourtune_norm_bwd")
+
+
+def fourtune_rope_init(D, axis_dims, theta=10000.0, layout=FT_ROPE_PAIRS,
+                       ladder=FT_ROPE_AXIS) -> FtRope:
+    rp = FtRope()
+    dims = (ctypes.c_int32 * max(len(axis_dims), 1))(*axis_dims)
+    _check(lib().fourtune_rope_init(ctypes.byref(rp), int(D), len(axis_dims), dims, float(theta),
+                                    int(layout), int(ladder)), "fourtune_rope_init")
+    return rp
+
+
+def rope_side(heads, inp, out, ld_in, ld_out, weight=None) -> FtRopeSide:
+    return FtRopeSide(int(heads), _ptr(inp), _ptr(out), int(ld_in), int(ld_out), _ptr(weight))
+
+
+def fourtune_rope_fwd(rp: FtRope, M, positions, eps, q: FtRopeSide, k: FtRopeSide, stream=None):
+    _check(lib().fourtune_rope_fwd(ctypes.byref(rp), int(M), _ptr(positions), float(eps),
+                                   ctypes.byref(q), ctypes.byref(k), _stream(stream)),
+           "fourtune_rope_fwd")
+
+
+def fourtune_rope_workspace_bytes(rp: FtRope, M) -> int:
+    return int(lib().fourtune_rope_workspace_bytes(ctypes.byref(rp), int(M)))
+
+
+def fourtune_rope_bwd(rp: FtRope, M, positions, eps, q: FtRopeSide, k: FtRopeSide, q_x, ld_qx, k_x,
+                      ld_kx, dq_weight, dk_weight, grad_dtype, workspace, ws_bytes, stream=None):
+    _check(lib().fourtune_rope_bwd(ctypes.byref(rp), int(M), _ptr(positions), float(eps),
+                                   ctypes.byref(q), ctypes.byref(k), _ptr(q_x), int(ld_qx),
+                                   _ptr(k_x), int(ld_kx), _ptr(dq_weight), _ptr(dk_weight),
+                                   int(grad_dtype), _ptr(workspace), int(ws_bytes),
+                                   _stream(stream)), "fourtune_rope_bwd")
+
+
+def fourtune_attn_fwd(d: FtAttn, q, k, v, o, lse, stream=None):
+    _check(lib().fourtune_attn_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                   _stream(stream)), "fourtune_attn_fwd")
+
+
+def fourtune_attn_workspace_bytes(d: FtAttn) -> int:
+    return int(lib().fourtune_attn_workspace_bytes(ctypes.byref(d)))
+
+
+def fourtune_attn_bwd(d: FtAttn, d_o, ld_do, q, k, v, o, lse, dq, ld_dq, dk, ld_dk, dv, ld_dv,
+                      workspace, ws_bytes, stream=None):
+    _check(lib().fourtune_attn_bwd(ctypes.byref(d), _ptr(d_o), int(ld_do), _ptr(q), _ptr(k),
+                                   _ptr(v), _ptr(o), _ptr(lse), _ptr(dq), int(ld_dq), _ptr(dk),
+                                   int(ld_dk), _ptr(dv), int(ld_dv), _ptr(workspace), int(ws_bytes),
+                                   _stream(stream)), "fourtune_attn_bwd")
+
+
+def fourtune_adamw_plan_bytes(tensors, n_tensors):
+    """(bytes of the table, elements of the state arenas) of an array of FtAdamwTensor."""
+    arena = ctypes.c_int64(0)
+    n = lib().fourtune_adamw_plan_bytes(tensors, int(n_tensors), ctypes.byref(arena))
+    return int(n), int(arena.value)
+
+
+def fourtune_adamw_plan(tensors, n_tensors, param_dtype, grad_dtype, state, host_table,
+                        table_bytes) -> FtAdamw:
+    d = FtAdamw()
+    _check(lib().fourtune_adamw_plan(tensors, int(n_tensors), int(param_dtype), int(grad_dtype),
+                                     int(state), ctypes.byref(d), _ptr(host_table),
+                                     int(table_bytes)), "fourtune_adamw_plan")
+    return d
+
+
+def fourtune_adamw_step(d: FtAdamw, t, lr, beta1, beta2, eps, weight_decay, seed, grad_scale=None,
+                        stream=None):
+    _check(lib().fourtune_adamw_step(ctypes.byref(d), int(t), float(lr), float(beta1), float(beta2),
+                                     float(eps), float(weight_decay), int(seed) & 0xFFFFFFFF,
+                                     _ptr(grad_scale), _stream(stream)), "fourtune_adamw_step")
 
 
 def fourtune_timing_enable(on: bool):

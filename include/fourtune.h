@@ -374,6 +374,243 @@ ft_status fourtune_act_fwd(int act, const uint16_t* h, int64_t n, uint16_t* out,
 ft_status fourtune_act_bwd(int act, const uint16_t* h, const uint16_t* g, int64_t n,
                            uint16_t* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the linears: what a DiT block computes between its quantized
+ * linears, and the optimizer step of the adapters.  The conventions at the
+ * top hold (device pointers, 16-byte aligned; one stream; every check before
+ * anything is enqueued), with two differences: row offsets are 64-bit, so
+ * tensors may pass 2^31 bytes, and every sum, softmax statistic, norm and
+ * gradient is accumulated in fp32 in a fixed order (the results do not
+ * depend on timing).
+ * ------------------------------------------------------------------------ */
+
+/* Normalization of a row x of C values, in fp32:
+ *   RMS:   n = x * rstd,           rstd = 1 / sqrt(mean(x^2) + eps)
+ *   LAYER: n = (x - mean) * rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps) */
+typedef enum { FT_NORM_NONE = 0, FT_NORM_RMS = 1, FT_NORM_LAYER = 2 } ft_norm_kind;
+
+/* The gated residual after one sub-block of a block and the modulated norm
+ * before the next one:
+ *   r = x + alpha * gate_b * (post_weight * N_post(y))       (x itself without y)
+ *   h = (1 + scale_b) * (weight * N(r)) + shift_b
+ * x: the residual stream, y: the sub-block's output, b: the sample a row
+ * belongs to.  r is rounded to the stream's type before N reads it.  Every
+ * factor is optional: a NULL weight, post_weight or gate is 1, a NULL scale
+ * or shift 0; post_norm NONE: N_post(y) = y.  Host struct; its pointers are
+ * device pointers.  Without y, the fields of r's formula are not read. */
+typedef struct {
+  int64_t M, C;             /* rows, channels: M >= 0, 8 <= C <= 16384, C % 8 == 0         */
+  int32_t n_seg;            /* samples, >= 1                                               */
+  int32_t stream_dtype;     /* FT_BF16 or FT_F32: x, r, dr, dx.  Everything else is bf16   */
+  const int32_t* seg;       /* device [n_seg + 1], ascending: sample b has the rows seg[b] ..
+                               seg[b+1] - 1 (it may have none).  Rows before seg[1] belong to
+                               the first sample, rows from seg[n_seg - 1] on to the last.
+                               NULL: samples of M / n_seg rows each (M % n_seg == 0)       */
+  int32_t norm, post_norm;  /* ft_norm_kind; norm is RMS or LAYER                          */
+  float eps, alpha;         /* eps >= 0 of both norms; the residual scale                  */
+  const uint16_t* weight;       /* bf16 [C]                                                */
+  const uint16_t* post_weight;  /* bf16 [C]                                                */
+  const uint16_t* scale;        /* bf16 [n_seg, C], rows ld_mod apart (the modulation      */
+  const uint16_t* shift;        /*   linear's output is one [n_seg, 6 C] tensor that holds */
+  const uint16_t* gate;         /*   several of them)                                      */
+  int64_t ld_mod;               /* elements, >= C, % 8 == 0                                */
+} ft_norm;
+
+/* Forward.  x [M, C], r [M, C] in the stream's type; y, h [M, C] bf16.
+ * y NULL: r = x; r may then be NULL (not written).  r may be x (in place).
+ * h NULL: only r is computed (the end of a block).  stats: optional fp32
+ * [M, 4], per row (mean, rstd) of r and (mean, rstd) of y (0, 1 where there
+ * is no such norm), for the backward.
+ * Errors: FT_EINVAL (NULLs, enums, eps), FT_ESHAPE, FT_EALIGN, FT_EDEVICE,
+ * FT_EUNSUPPORTED.  M == 0 is a no-op. */
+ft_status fourtune_norm_fwd(const ft_norm* d, const void* x, const uint16_t* y, void* r,
+                            uint16_t* h, float* stats, void* stream);
+
+/* Backward.  dh [M, C] bf16: the gradient of h (NULL: none; then r and the
+ * norm's fields are not read); dr [M, C]: the gradient of r from what else
+ * reads it (NULL: none); at least one of the two.  r, y, stats: of the
+ * forward (y NULL as there; stats required where a norm is differentiated).
+ *   dx [M, C] (stream type, may be dr): the gradient of r, and so of x
+ *   dy [M, C] bf16 (with y)
+ *   dscale, dshift, dgate [n_seg, C], rows ld_dmod apart; dweight,
+ *   dpost_weight [C]: optional outputs in grad_dtype, sums over the rows of a
+ *   sample or over all rows (zeros for a sample without rows).  dscale,
+ *   dshift and dweight need dh; dgate and dpost_weight need y.
+ * workspace: fourtune_norm_workspace_bytes(d) bytes (0 for invalid shapes);
+ * not needed (NULL) when none of the five is asked for.
+ * Errors: as the forward, and FT_EWORKSPACE. */
+size_t fourtune_norm_workspace_bytes(const ft_norm* d);
+ft_status fourtune_norm_bwd(const ft_norm* d, const uint16_t* dh, const void* dr, const void* r,
+                            const uint16_t* y, const float* stats, void* dx, uint16_t* dy,
+                            void* dscale, void* dshift, void* dgate, int64_t ld_dmod,
+                            void* dweight, void* dpost_weight, ft_dtype grad_dtype,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* Rotary positions with several axes (time, height, width, ...), with an
+ * optional RMS norm of every query and key head before the rotation:
+ *   t = w * x / sqrt(mean(x^2) + eps)    over the D values of a head (w given), else t = x
+ *   (out_a, out_b) = (t_a cos - t_b sin, t_a sin + t_b cos)   for the pair (a, b) = pair j,
+ *   angle = position[axis(j)] * freq(j);  the D - 2 n_pairs values past the pairs pass through
+ * A row holds its heads one after the other, D values each. */
+#define FT_ROPE_MAX_AXES 4
+#define FT_ROPE_MAX_DIM 256
+typedef enum {
+  FT_ROPE_PAIRS = 0,   /* pair j is the values 2j and 2j + 1 of a head              */
+  FT_ROPE_HALVES = 1   /* pair j is the values j and j + n_pairs; n_pairs % 8 == 0  */
+} ft_rope_layout;
+typedef enum {
+  FT_ROPE_AXIS = 0,    /* freq(j) = theta^(-2 i / axis_dim): every axis has its own
+                          frequencies, i counts its pairs                              */
+  FT_ROPE_SHARED = 1   /* freq(j) = theta^(-j / n_pairs): one run of frequencies that
+                          the axes divide between them                                 */
+} ft_rope_ladder;
+
+/* Filled by fourtune_rope_init and then only read. */
+typedef struct {
+  int32_t D, n_axes, layout, n_pairs;
+  int32_t axis[FT_ROPE_MAX_DIM / 2];       /* axis of pair j                                     */
+  float turn_hi[FT_ROPE_MAX_DIM / 2];      /* freq(j) / 2 pi as the sum of two fp32: the angle   */
+  float turn_lo[FT_ROPE_MAX_DIM / 2];      /*   in turns keeps its fraction at large positions   */
+} ft_rope;
+
+/* Axis i rotates axis_dims[i] values of each head (even, >= 2); they take
+ * pairs in order, together 2 n_pairs <= D values.  D % 8 == 0, 8 <= D <= 256,
+ * 1 <= n_axes <= 4, theta > 0.  Errors: FT_EINVAL, FT_ESHAPE. */
+ft_status fourtune_rope_init(ft_rope* rp, int32_t D, int32_t n_axes, const int32_t* axis_dims,
+                             double theta, int32_t layout, int32_t ladder);
+
+/* One side (queries or keys) of the rotation. */
+typedef struct {
+  int32_t heads;            /* >= 0: 0 leaves the side out                                 */
+  const uint16_t* in;       /* bf16 [M, heads * D], rows ld_in apart (% 8 == 0)            */
+  uint16_t* out;            /* bf16, rows ld_out apart; may be `in` with ld_in (in place)  */
+  int64_t ld_in, ld_out;
+  const uint16_t* weight;   /* bf16 [D] of the norm, NULL: no norm                         */
+} ft_rope_side;
+
+/* Forward: positions int32 [M, n_axes] (|position| <= 2^24), eps >= 0.
+ * Errors: FT_EINVAL, FT_ESHAPE (M < 0 or > 2^30), FT_EALIGN, FT_EDEVICE,
+ * FT_EUNSUPPORTED.  M == 0 is a no-op. */
+ft_status fourtune_rope_fwd(const ft_rope* rp, int64_t M, const int32_t* positions, float eps,
+                            const ft_rope_side* q, const ft_rope_side* k, void* stream);
+
+/* Backward of one call of the forward.  Each side's `in` is the gradient of
+ * the forward's output and `out` the gradient of its input (in place
+ * allowed), `weight` as in the forward; q_x, k_x: the forward's inputs, rows
+ * ld_qx, ld_kx apart, needed where the side has a weight (else NULL).
+ * dq_weight, dk_weight [D] in grad_dtype: optional gradients of the weights.
+ * workspace: fourtune_rope_workspace_bytes(rp, M) bytes, not needed without
+ * them.  Errors: as the forward, and FT_EWORKSPACE. */
+size_t fourtune_rope_workspace_bytes(const ft_rope* rp, int64_t M);
+ft_status fourtune_rope_bwd(const ft_rope* rp, int64_t M, const int32_t* positions, float eps,
+                            const ft_rope_side* q, const ft_rope_side* k, const uint16_t* q_x,
+                            int64_t ld_qx, const uint16_t* k_x, int64_t ld_kx, void* dq_weight,
+                            void* dk_weight, ft_dtype grad_dtype, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* Attention inside packed documents.  Query i and key j of one document:
+ *   s_ij = scale * q_i . k_j ;  with softcap c > 0: s_ij = c tanh(s_ij / c)
+ *   p_ij = exp(s_ij - lse_i) over the keys j that i sees,  lse_i = log sum exp s_ij
+ *   o_i = sum_j p_ij v_j
+ * FULL: a query sees its whole document.  CAUSAL: the keys up to itself.
+ * PREFIX: the keys up to itself and the document's first prefix[d] keys.
+ * Query head h reads key head h * Hkv / Hq (Hq % Hkv == 0).  A document's
+ * result depends on its own rows only, whatever the others hold (NaN and Inf
+ * too), and rows in no document are not read: they get o = 0, lse = -inf and
+ * zero gradients. */
+typedef enum { FT_MASK_FULL = 0, FT_MASK_CAUSAL = 1, FT_MASK_PREFIX = 2 } ft_attn_mask;
+typedef struct {
+  int64_t M;                /* rows of q, k, v, o: 0 <= M <= 2^30                          */
+  int32_t Hq, Hkv, D;       /* heads of queries and of keys and values; D = 64 or 128      */
+  int32_t mask;             /* ft_attn_mask                                                */
+  float scale, softcap;     /* scale > 0; softcap >= 0 (0: none)                           */
+  int32_t n_doc;            /* documents, >= 1                                             */
+  const int32_t* doc;       /* device [n_doc + 1], ascending: document d has the rows doc[d]
+                               .. doc[d+1] - 1 (it may have none); NULL: one document of
+                               all rows (n_doc == 1)                                       */
+  const int32_t* prefix;    /* device [n_doc], PREFIX only (clamped to the document)       */
+  int64_t ld_q, ld_k, ld_v, ld_o;   /* elements between rows, % 8 == 0; a row holds its heads
+                               one after the other, D values each                          */
+} ft_attn;
+
+/* Forward: q, k, v -> o (bf16) and lse (fp32 [Hq, M], NULL: not written).
+ * Errors: FT_EINVAL, FT_ESHAPE, FT_EALIGN, FT_EDEVICE, FT_EUNSUPPORTED.
+ * M == 0 is a no-op. */
+ft_status fourtune_attn_fwd(const ft_attn* d, const uint16_t* q, const uint16_t* k,
+                            const uint16_t* v, uint16_t* o, float* lse, void* stream);
+
+/* Backward: d_o (rows ld_do apart) and the forward's q, k, v, o, lse ->
+ * dq, dk, dv (rows ld_dq, ld_dk, ld_dv apart; they may be parts of one
+ * tensor).  workspace: fourtune_attn_workspace_bytes(d) bytes (0 for invalid
+ * shapes).  Errors: as the forward, and FT_EWORKSPACE. */
+size_t fourtune_attn_workspace_bytes(const ft_attn* d);
+ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do,
+                            const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                            const uint16_t* o, const float* lse, uint16_t* dq, int64_t ld_dq,
+                            uint16_t* dk, int64_t ld_dk, uint16_t* dv, int64_t ld_dv,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* AdamW over many tensors in one launch.  For every element, step t >= 1, in
+ * fp32 with one rounding per operation:
+ *   g' = grad_scale * g
+ *   m = beta1 m + (1 - beta1) g'        v = beta2 v + (1 - beta2) g'^2
+ *   p = (1 - lr wd) p - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * Parameters: FT_F32; FT_BF16 with an fp32 master (the master is stepped and
+ * p gets it rounded to nearest); or FT_BF16 alone, rounded at random (a step
+ * smaller than half a bf16 step is kept on average instead of lost).
+ * States, in arenas where tensor i starts at the sum of the earlier tensors'
+ * sizes, each rounded up to 128:
+ *   FT_STATE_F32: m and v, 4 bytes each;
+ *   FT_STATE_Q8: 1 byte each and an fp32 scale per 128 elements, the block's
+ *     largest magnitude.  A code has 4 fraction bits; code c with exponent
+ *     field e = c / 16 and fraction f = c % 16 stands for u(c) = f (e = 0) or
+ *     (16 + f) 2^(e-1) in units of scale / u(largest).  m: a sign bit and 3
+ *     exponent bits; v: its root, 4 exponent bits (the root halves the range
+ *     that a code has to span, and a root above 0 never rounds to 0, so no
+ *     step is divided by eps alone).  Codes are rounded at random: with a
+ *     rounding to nearest a decay of v by 0.1% a step would never move a code.
+ * Random rounding adds 16 or 19 bits below the last kept one, from a mix of
+ * the element's place in the arena with (seed, t): the same call gives the
+ * same bits. */
+typedef enum { FT_STATE_F32 = 0, FT_STATE_Q8 = 1 } ft_state;
+typedef struct {
+  void* p;                  /* parameter, param_dtype                      */
+  const void* g;            /* gradient, grad_dtype                        */
+  float* master;            /* fp32 master, or NULL (all tensors alike)    */
+  int64_t n;                /* elements, >= 0                              */
+} ft_adamw_tensor;
+typedef struct {
+  int32_t n_tensors;
+  int32_t param_dtype, grad_dtype, state;   /* ft_dtype, ft_dtype, ft_state */
+  int32_t has_master;
+  int64_t arena;            /* elements of the state arenas                */
+  int64_t n_chunks;         /* filled by fourtune_adamw_plan               */
+  void* m;                  /* fp32 [arena], or codes uint8 [arena]        */
+  void* v;
+  float* m_scale;           /* fp32 [arena / 128], FT_STATE_Q8 only        */
+  float* v_scale;
+  const void* table;        /* device copy of the table                    */
+} ft_adamw;
+
+/* The table of a set of tensors, made once: fourtune_adamw_plan_bytes gives
+ * its size (0 if a tensor is invalid) and the arenas' elements;
+ * fourtune_adamw_plan checks the tensors, fills `host_table` (host memory)
+ * and d's n_tensors, has_master, arena and n_chunks.  The caller copies the table to the
+ * device, sets d->table, d->m .. d->v_scale, and keeps all of them.
+ * arena < 2^32.  Errors: FT_EINVAL, FT_ESHAPE, FT_EALIGN. */
+size_t fourtune_adamw_plan_bytes(const ft_adamw_tensor* tensors, int32_t n_tensors,
+                                 int64_t* arena);
+ft_status fourtune_adamw_plan(const ft_adamw_tensor* tensors, int32_t n_tensors,
+                              int32_t param_dtype, int32_t grad_dtype, int32_t state,
+                              ft_adamw* d, void* host_table, size_t table_bytes);
+
+/* One step.  grad_scale: optional device float (a clipping factor), NULL: 1.
+ * Requirements: t >= 1, 0 <= beta < 1, eps > 0.
+ * Errors: FT_EINVAL, FT_EALIGN, FT_EDEVICE, FT_EUNSUPPORTED. */
+ft_status fourtune_adamw_step(const ft_adamw* d, int64_t t, double lr, double beta1, double beta2,
+                              double eps, double weight_decay, uint32_t seed,
+                              const float* grad_scale, void* stream);
+
 /* Static, human-readable text for a status code. */
 const char* fourtune_status_string(ft_status s);
 

@@ -52,10 +52,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
   const int nt = (seen + BN - 1) / BN;
   const uint16_t* kp = a.k + static_cast<int64_t>(dt.lo) * a.ld_k + kvh * D;
   const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
+  const uint32_t lane0 = stage_lane<D>(lane);
   auto fetch = [&](int t) {
     uint8_t* buf = lds + (t & 1) * 2 * TB;
-    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane);
-    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane);
+    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane, lane0);
+    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane,
+                    lane0);
   };
   fetch(0);
   u32x4 q[KS];
@@ -67,14 +69,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
       if (live) q[ks] = reinterpret_cast<const u32x4*>(qrow)[2 * ks + half];
     }
   }
-  uint32_t koff[KS], voff[DB][2];
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) koff[ks] = row_off<D>(l32, half, ks);
-#pragma unroll
-  for (int db = 0; db < DB; ++db)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) voff[db][i] = col_off<D>(lane, db, i);
-
+  const uint32_t kbase = row_base<D>(l32, half), vbase = col_base<D>(lane);
   f32x16 o[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) o[db] = zero16();
@@ -94,7 +89,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
       s[kb] = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        s[kb] = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + koff[ks]), q[ks], s[kb]);
+        s[kb] = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + (kbase ^ row_step(ks))), q[ks], s[kb]);
     }
     if constexpr (CAP) {
 #pragma unroll
@@ -104,13 +99,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
     }
     const int last = t * BN + BN - 1;
     if (last >= len || (a.mask != 0 && last > wq0 && last >= dt.prefix)) {
-      // keys from `end` on are hidden from this lane's query
-      const int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
+      // the tile's keys from `end` on are hidden from this lane's query
+      const int end = (a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix))) - t * BN - 4 * half;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (t * BN + kb * 32 + acc_row(r, half) >= end) s[kb][r] = kNegInf;
+          if (kb * 32 + acc_row(r) >= end) s[kb][r] = kNegInf;
     }
     float mt = s[0][0];
 #pragma unroll
@@ -147,7 +142,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
         const uint8_t* vk = vt + (kb * 32 + h * 16) * 2 * D;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
-          o[db] = mfma_bf16_32x32x16(col_read(vk, voff[db][0], voff[db][1]), p, o[db]);
+          o[db] = mfma_bf16_32x32x16(col_read(vk, vbase ^ col_step<D>(db, 0), vbase ^ col_step<D>(db, 1)), p, o[db]);
       }
     }
     staged_barrier();

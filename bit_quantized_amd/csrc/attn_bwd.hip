@@ -3,6 +3,10 @@
 //   dP = dO V^T,  dS = P (dP - delta) scale [(1 - tanh^2)],
 //   dQ = dS K,  dK = dS^T Q,  dV = P^T dO
 //
+// delta_i is also sum_j p_ij dP_ij.  do . o is one pass less but has the
+// rounding of o in it, which shows where a query sees few keys (an o as large
+// as the values); there (up to 256 keys) the sum over the keys is taken.
+//
 // Two kernels, so that every sum has one owner and a fixed order (no
 // atomics): k_attn_dq walks the keys of 128 queries and also leaves delta;
 // k_attn_dkv walks the queries of 128 keys, over all query heads of the key
@@ -20,23 +24,20 @@ using namespace attn_dev;
 namespace {
 
 constexpr int BM = 128;
+constexpr int kFewTiles = 4;             // of 64 keys
 
-// ds = p (dp - delta) [slope]; p from the score s and lse2 = lse / ln 2.
+// A score s to t, with p = exp2(t); `slope` is the cap's derivative there.
+// lse2 = lse / ln 2.
 template <bool CAP>
-__device__ __forceinline__ void p_and_ds(float s, float dp, float lse2, float delta, float c1,
-                                         float c2, bool hidden, float& p, float& ds) {
-  float slope = 1.0f;
-  float t;
+__device__ __forceinline__ float score(float s, float lse2, float c1, float c2, float& slope) {
   if constexpr (CAP) {
     const float th = tanh_f32(s * c1);
-    t = __builtin_fmaf(c2, th, -lse2);
-    slope = 1.0f - th * th;
+    slope = __builtin_fmaf(-th, th, 1.0f);
+    return __builtin_fmaf(c2, th, -lse2);
   } else {
-    t = __builtin_fmaf(s, c1, -lse2);
+    slope = 1.0f;
+    return __builtin_fmaf(s, c1, -lse2);
   }
-  p = hidden ? 0.0f : __builtin_amdgcn_exp2f(t);
-  ds = p * (dp - delta);
-  if constexpr (CAP) ds *= slope;
 }
 
 template <int D, bool CAP>
@@ -67,10 +68,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(const AttnArgs a, uint32_t t
   const int nt = (seen + BN - 1) / BN;
   const uint16_t* kp = a.k + static_cast<int64_t>(dt.lo) * a.ld_k + kvh * D;
   const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
+  const uint32_t lane0 = stage_lane<D>(lane);
   auto fetch = [&](int t) {
     uint8_t* buf = lds + (t & 1) * 2 * TB;
-    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane);
-    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane);
+    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane, lane0);
+    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane, lane0);
   };
   fetch(0);
   u32x4 q[KS], g[KS];
@@ -94,26 +96,50 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(const AttnArgs a, uint32_t t
       }
     }
     delta = halves_sum(delta);
-    if (live) {
-      lse2 = a.lse[head * a.M + qi] * kLog2e;
-      if (half == 0) a.delta[head * a.M + qi] = delta;
-    }
+    if (live) lse2 = a.lse[head * a.M + qi] * kLog2e;
   }
-  uint32_t koff[KS], coff[DB][2];
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) koff[ks] = row_off<D>(l32, half, ks);
-#pragma unroll
-  for (int db = 0; db < DB; ++db)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) coff[db][i] = col_off<D>(lane, db, i);
+  const uint32_t rbase = row_base<D>(l32, half), cbase = col_base<D>(lane);
   f32x16 acc[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) acc[db] = zero16();
   const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
   const float c2 = a.softcap * kLog2e;
   const int wq0 = q0 + wave * 32;
-  const int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
+  int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
   staged_barrier();
+  if (nt <= kFewTiles) {
+    // delta = sum p dP / sum p, by a pass over the keys of its own
+    float psum = 0.0f, pdp = 0.0f;
+    for (int t = 0; t < nt; ++t) {
+      if (t + 1 < nt) fetch(t + 1);
+      const uint8_t* kt = lds + (t & 1) * 2 * TB;
+      for (int kb = 0; kb < 2; ++kb) {
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t at = kb * 32 * 2 * D + (rbase ^ row_step(ks));
+          s = mfma_bf16_32x32x16(lds_read_b128(kt + at), q[ks], s);
+          dp = mfma_bf16_32x32x16(lds_read_b128(kt + TB + at), g[ks], dp);
+        }
+        const int e = end - t * BN - kb * 32 - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float slope;
+          const float x = score<CAP>(s[r], lse2, c1, c2, slope);
+          const float p = acc_row(r) < e ? __builtin_amdgcn_exp2f(x) : 0.0f;
+          psum += p;
+          pdp = __builtin_fmaf(p, dp[r], pdp);
+        }
+      }
+      staged_barrier();
+    }
+    delta = halves_sum(pdp) / halves_sum(psum);
+    // one key: p = 1 whatever the scores, and nothing of them is left in dS
+    if (end == 1) end = 0;
+    fetch(0);
+    staged_barrier();
+  }
+  if (live && half == 0) a.delta[head * a.M + qi] = delta;
   for (int t = 0; t < nt; ++t) {
     if (t + 1 < nt) fetch(t + 1);
     const uint8_t* kt = lds + (t & 1) * 2 * TB;
@@ -125,23 +151,30 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(const AttnArgs a, uint32_t t
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        s = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + koff[ks]), q[ks], s);
-        dp = mfma_bf16_32x32x16(lds_read_b128(vt + kb * 32 * 2 * D + koff[ks]), g[ks], dp);
+        s = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + (rbase ^ row_step(ks))), q[ks], s);
+        dp = mfma_bf16_32x32x16(lds_read_b128(vt + kb * 32 * 2 * D + (rbase ^ row_step(ks))), g[ks], dp);
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const bool hidden = edge && t * BN + kb * 32 + acc_row(r, half) >= end;
-        float p, ds;
-        p_and_ds<CAP>(s[r], dp[r], lse2, delta, c1, c2, hidden, p, ds);
-        s[r] = ds;
+        float slope;
+        s[r] = score<CAP>(s[r], lse2, c1, c2, slope);
+        dp[r] = CAP ? (dp[r] - delta) * slope : dp[r] - delta;
       }
+      if (edge) {
+        const int e = end - t * BN - kb * 32 - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (acc_row(r) >= e) s[r] = kNegInf;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r]) * dp[r];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4 d = pack8(s, 8 * h);
         const uint8_t* kk = kt + (kb * 32 + h * 16) * 2 * D;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
-          acc[db] = mfma_bf16_32x32x16(col_read(kk, coff[db][0], coff[db][1]), d, acc[db]);
+          acc[db] = mfma_bf16_32x32x16(col_read(kk, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1)), d, acc[db]);
       }
     }
     staged_barrier();
@@ -159,12 +192,15 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(const AttnArgs a, uint32_t t
   }
 }
 
-// 128 keys of one key head; a wave owns 32.
-template <int D, bool CAP>
-__global__ __launch_bounds__(256, 1) void k_attn_dkv(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32, BQ = 64;
+// 32 NW keys of one key head; a wave owns 32.  Two accumulators of 32 keys by D
+// take half the registers, so V is read from LDS (its rows there stay for the
+// whole walk) and two waves fit on a SIMD.
+template <int D, bool CAP, int NW, int BQ>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint32_t tiles) {
+  constexpr int KS = D / 16, DB = D / 32, BM = 32 * NW;
   constexpr int TB = BQ * D * 2;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TB];       // [buffer][Q, dO]
+  __shared__ __attribute__((aligned(16))) uint8_t vlds[BM * D * 2];
   __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];     // [buffer][lse2, delta]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
@@ -193,107 +229,122 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(const AttnArgs a, uint32_t 
   const int nt = (len + BQ - 1) / BQ - first;
   const int group = a.Hq / a.Hkv;
   const int total = nt * group;                          // (query head, tile) pairs
-  auto fetch = [&](int it) {
-    const int h = kvh * group + it / nt;
-    const int t = first + it % nt;
+  const uint32_t lane0 = stage_lane<D>(lane);
+  auto fetch = [&](int it, int h, int t) {
     uint8_t* buf = lds + (it & 1) * 2 * TB;
     const int64_t row = dt.lo + static_cast<int64_t>(t) * BQ;
-    stage<D, BQ, 4>(a.q + row * a.ld_q + h * D, a.ld_q, len - t * BQ, buf, wave, lane);
-    stage<D, BQ, 4>(a.d_o + row * a.ld_do + h * D, a.ld_do, len - t * BQ, buf + TB, wave, lane);
+    stage<D, BQ, NW>(a.q + row * a.ld_q + h * D, a.ld_q, len - t * BQ, buf, wave, lane, lane0);
+    stage<D, BQ, NW>(a.d_o + row * a.ld_do + h * D, a.ld_do, len - t * BQ, buf + TB, wave, lane, lane0);
   };
-  // lse and delta of a tile, through registers (rows past the end: p = 0)
+  // lse and delta of a tile, through registers: the first 64 threads have
+  // lse (rows past the end: inf, so p = 0), the next 64 delta
   float nstat = 0.0f;
-  auto fetch_stat = [&](int it) {
+  auto fetch_stat = [&](int h, int t) {
     if (threadIdx.x < 2 * BQ) {
-      const int h = kvh * group + it / nt;
-      const int i = threadIdx.x & (BQ - 1), t = first + it % nt;
-      const bool in = t * BQ + i < len;
-      const int64_t at = h * a.M + dt.lo + t * BQ + i;
-      if (threadIdx.x < BQ) nstat = in ? a.lse[at] * kLog2e : __builtin_inff();
-      else nstat = in ? a.delta[at] : 0.0f;
+      uint32_t i = threadIdx.x & (BQ - 1);
+      in_place(i);
+      const float* p = threadIdx.x < BQ ? a.lse : a.delta;
+      nstat = threadIdx.x < BQ ? __builtin_inff() : 0.0f;
+      if (t * BQ + static_cast<int>(i) < len) nstat = p[h * a.M + dt.lo + t * BQ + i];
     }
   };
   auto put_stat = [&](int it) {
-    if (threadIdx.x < 2 * BQ) stat[it & 1][threadIdx.x / BQ][threadIdx.x & (BQ - 1)] = nstat;
+    if (threadIdx.x < 2 * BQ)
+      stat[it & 1][threadIdx.x / BQ][threadIdx.x & (BQ - 1)] = threadIdx.x < BQ ? nstat * kLog2e : nstat;
   };
-  fetch(0);
-  fetch_stat(0);
-  u32x4 k[KS], v[KS];
+  int t = first, nh = kvh * group, ntile = first;        // this tile; the next one's head and tile
+  stage<D, BM, NW>(a.v + static_cast<int64_t>(dt.row0) * a.ld_v + kvh * D, a.ld_v, dt.rows, vlds, wave, lane,
+                   lane0);
+  fetch(0, nh, ntile);
+  fetch_stat(nh, ntile);
+  u32x4 k[KS];
   {
     const u32x4* krow = reinterpret_cast<const u32x4*>(a.k + static_cast<int64_t>(kj) * a.ld_k + kvh * D);
-    const u32x4* vrow = reinterpret_cast<const u32x4*>(a.v + static_cast<int64_t>(kj) * a.ld_v + kvh * D);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      k[ks] = v[ks] = u32x4{0, 0, 0, 0};
-      if (live) {
-        k[ks] = krow[2 * ks + half];
-        v[ks] = vrow[2 * ks + half];
-      }
+      k[ks] = u32x4{0, 0, 0, 0};
+      if (live) k[ks] = krow[2 * ks + half];
     }
   }
-  uint32_t roff[KS], coff[DB][2];
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) roff[ks] = row_off<D>(l32, half, ks);
-#pragma unroll
-  for (int db = 0; db < DB; ++db)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) coff[db][i] = col_off<D>(lane, db, i);
+  uint32_t rbase = row_base<D>(l32, half), cbase = col_base<D>(lane);
   f32x16 dk[DB], dv[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
   const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
   const float c2 = a.softcap * kLog2e;
   const int wk0 = k0 + wave * 32;                        // the wave's first key
-  const int key = wk0 + l32;
+  const bool one_key = len == 1 || (a.mask != 0 && dt.prefix <= 1);        // the first query does
+  const int first_seen = wk0 + l32 >= dt.prefix ? wk0 + l32 : 0;   // queries from here on see the key
+  const uint8_t* vl = vlds + wave * 32 * 2 * D;
   put_stat(0);
   staged_barrier();
   for (int it = 0; it < total; ++it) {
+    in_place(rbase);
+    in_place(cbase);
+    if (++ntile == first + nt) {
+      ntile = first;
+      ++nh;
+    }
     if (it + 1 < total) {
-      fetch(it + 1);
-      fetch_stat(it + 1);
+      fetch(it + 1, nh, ntile);
+      fetch_stat(nh, ntile);
     }
     const uint8_t* qt = lds + (it & 1) * 2 * TB;
     const uint8_t* gt = qt + TB;
     const float* ls = stat[it & 1][0];
     const float* de = stat[it & 1][1];
-    const int t = first + it % nt;
     // some query of the tile does not see some key of the wave
     const bool edge = a.mask != 0 && t * BQ < wk0 + 31 && wk0 + 31 >= dt.prefix;
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < BQ / 32; ++qb) {
+      __builtin_amdgcn_sched_barrier(0);
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        s = mfma_bf16_32x32x16(lds_read_b128(qt + qb * 32 * 2 * D + roff[ks]), k[ks], s);
-        dp = mfma_bf16_32x32x16(lds_read_b128(gt + qb * 32 * 2 * D + roff[ks]), v[ks], dp);
+        s = mfma_bf16_32x32x16(lds_read_b128(qt + qb * 32 * 2 * D + (rbase ^ row_step(ks))), k[ks], s);
+        dp = mfma_bf16_32x32x16(lds_read_b128(gt + qb * 32 * 2 * D + (rbase ^ row_step(ks))),
+                                lds_read_b128(vl + (rbase ^ row_step(ks))), dp);
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f32x4 lse2 = *reinterpret_cast<const f32x4*>(ls + qb * 32 + 8 * j + 4 * half);
         const f32x4 delta = *reinterpret_cast<const f32x4*>(de + qb * 32 + 8 * j + 4 * half);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 4 * j + e;
-          const int query = t * BQ + qb * 32 + 8 * j + 4 * half + e;
-          const bool hidden = edge && key > query && key >= dt.prefix;
-          float p, ds;
-          p_and_ds<CAP>(s[r], dp[r], lse2[e], delta[e], c1, c2, hidden, p, ds);
-          s[r] = p;
-          dp[r] = ds;
+          float slope;
+          s[4 * j + e] = score<CAP>(s[4 * j + e], lse2[e], c1, c2, slope);
+          dp[4 * j + e] = CAP ? (dp[4 * j + e] - delta[e]) * slope : dp[4 * j + e] - delta[e];
         }
       }
+      if (edge) {
+        // key > query: hidden, unless in the prefix
+        const int e = first_seen - t * BQ - qb * 32 - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (acc_row(r) < e) s[r] = kNegInf;
+      }
+      // a query that sees one key has p = 1 and dS = 0
+      if (one_key && t == 0 && qb == 0 && half == 0) dp[0] = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[r] = __builtin_amdgcn_exp2f(s[r]);
+        dp[r] *= s[r];
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4 pp = pack8(s, 8 * h), dd = pack8(dp, 8 * h);
         const uint32_t at = (qb * 32 + h * 16) * 2 * D;
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
-          dv[db] = mfma_bf16_32x32x16(col_read(gt + at, coff[db][0], coff[db][1]), pp, dv[db]);
-          dk[db] = mfma_bf16_32x32x16(col_read(qt + at, coff[db][0], coff[db][1]), dd, dk[db]);
+          dv[db] = mfma_bf16_32x32x16(col_read(gt + at, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1)), pp, dv[db]);
+          dk[db] = mfma_bf16_32x32x16(col_read(qt + at, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1)), dd, dk[db]);
         }
       }
     }
     if (it + 1 < total) put_stat(it + 1);
+    t = ntile;
     staged_barrier();
   }
   if (live) {
@@ -316,13 +367,15 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(const AttnArgs a, uint32_t 
 
 hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>(tiles_of<BM>(a));
+  constexpr int NWK = 4, BQK = 32;
+  const uint32_t ktiles = static_cast<uint32_t>(tiles_of<32 * NWK>(a));
 #define FT_AB(DD, C)                                                                              \
   do {                                                                                            \
     hipLaunchKernelGGL((k_attn_dq<DD, C>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(256),  \
                        0, st, a, tiles);                                                          \
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;                              \
-    hipLaunchKernelGGL((k_attn_dkv<DD, C>), dim3(tiles * static_cast<uint32_t>(a.Hkv)),           \
-                       dim3(256), 0, st, a, tiles);                                               \
+    hipLaunchKernelGGL((k_attn_dkv<DD, C, NWK, BQK>), dim3(ktiles * static_cast<uint32_t>(a.Hkv)), \
+                       dim3(64 * NWK), 0, st, a, ktiles);                                         \
   } while (0)
   if (D == 128) { if (a.softcap > 0) FT_AB(128, true); else FT_AB(128, false); }
   else { if (a.softcap > 0) FT_AB(64, true); else FT_AB(64, false); }

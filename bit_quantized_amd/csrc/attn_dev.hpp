@@ -12,6 +12,18 @@ namespace attn_dev {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -__builtin_inff();
 
+// A value that is the same in all lanes, told to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(x)));
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = uniform(static_cast<uint32_t>(v)), hi = uniform(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const T*>(hi << 32 | lo);
+}
+
 // The rows of one tile: [row0, row0 + rows) of the document [lo, hi), whose
 // queries see keys lo .. (mask); keys = false: rows of no document.
 struct DocTile {
@@ -75,8 +87,11 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int t, DocTile& o) 
       base += __builtin_amdgcn_readlane(scan, 63);
     }
   }
+  o.lo = uniform(o.lo);
+  o.hi = uniform(o.hi);
+  o.row0 = uniform(o.row0);
   o.rows = min(BM, o.hi - o.row0);
-  o.prefix = max(0, min(o.prefix, o.hi - o.lo));
+  o.prefix = max(0, min(uniform(o.prefix), o.hi - o.lo));
   return true;
 }
 template <int BM>
@@ -93,6 +108,10 @@ __device__ __forceinline__ uint32_t swz(uint32_t row) {
   return D == 128 ? ((row & 3u) << 2) | ((row >> 2) & 3u) : ((row & 2u) << 1) | ((row >> 2) & 3u);
 }
 
+// Keeps what is computed from x inside the loop that it is used in, instead
+// of in registers across it.
+__device__ __forceinline__ void in_place(uint32_t& x) { asm volatile("" : "+v"(x)); }
+
 // The LDS destination goes in as an opaque address, so that the compiler
 // does not wait for all loads in flight before the next LDS read; the
 // kernels wait themselves (vmcnt, then a barrier) before a tile is read.
@@ -103,43 +122,62 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, ui
                                            (int)off, 0, 0, 0);
 }
 // Start the loads of ROWS rows of D bf16 (the first at p, ld elements apart)
-// into `tile`, by NW waves; rows from `have` on become zeros.
+// into `tile`, by NW waves; rows from `have` on become zeros (the resource
+// ends with row have - 1, and every row is at least D elements long).  `lane0`
+// is stage_lane()'s: a lane's place in its instruction's rows.
+template <int D>
+__device__ __forceinline__ uint32_t stage_lane(int lane) {
+  constexpr int CH = D / 8;                    // chunks of a row
+  return ((lane % CH) ^ swz<D>(lane / CH)) << 4;
+}
 template <int D, int ROWS, int NW>
 __device__ __forceinline__ void stage(const uint16_t* p, int64_t ld, int have, uint8_t* tile,
-                                      int wave, int lane) {
-  constexpr int CH = D / 8;                    // chunks of a row
+                                      int wave, int lane, uint32_t lane0) {
+  constexpr int CH = D / 8;
   constexpr int RI = 64 / CH;                  // rows of one instruction
   constexpr int N = ROWS / RI / NW;            // instructions of a wave
   static_assert(N * RI * NW == ROWS, "the waves share the tile evenly");
-  const __amdgpu_buffer_rsrc_t r = make_rsrc(p, 0x7FFFFFFFu);
+  const uint32_t row_bytes = static_cast<uint32_t>(ld) * 2u;
+  const uint32_t rows = static_cast<uint32_t>(have < 0 ? 0 : have < ROWS ? have : ROWS);
+  const __amdgpu_buffer_rsrc_t r = make_rsrc(uniform(p), uniform(rows * row_bytes));
+  in_place(lane0);
+  const uint32_t at = static_cast<uint32_t>(lane / CH) * row_bytes;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int first = (wave * N + i) * RI;
-    const int row = first + lane / CH;
-    const uint32_t c = (lane % CH) ^ swz<D>(row);
-    const uint32_t off = static_cast<uint32_t>(row) * static_cast<uint32_t>(ld) * 2u + c * 16u;
-    dma16(r, tile + first * (2 * D), row < have ? off : BUF_OOB);
+    // (row = first + lane / CH, in separate bits, and swz is linear in them)
+    const uint32_t flip = swz<D>(static_cast<uint32_t>(first)) << 4;
+    dma16(r, tile + first * (2 * D), at + static_cast<uint32_t>(first) * row_bytes + (lane0 ^ flip));
   }
 }
 __device__ __forceinline__ void staged_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Byte offset in a tile of the row operand of step ks (16 values of D): lane
-// l has values 16 ks + 8 (l / 32) .. +7 of row l % 32.
+// Byte offsets in a tile.  The permutation is an exclusive or, and rows and
+// chunks are bit fields of the offset, so every offset of a lane is one base
+// xor a constant.
+// Row operand of step ks (16 values of D): lane l has values 16 ks + 8 (l /
+// 32) .. +7 of row l % 32:  row_base() ^ row_step(ks).
 template <int D>
-__device__ __forceinline__ uint32_t row_off(int l32, int half, int ks) {
-  return l32 * (2 * D) + (((2 * ks + half) ^ swz<D>(l32)) << 4);
+__device__ __forceinline__ uint32_t row_base(int l32, int half) {
+  return l32 * (2 * D) + ((half ^ swz<D>(l32)) << 4);
 }
-// Byte offset of half i of the column operand of the first 16 rows: lane l
-// gets, through the transposing read, rows 4 (l / 32) + 8 i .. +3 of column
-// 32 db + l % 32; the two halves give the eight rows that the accumulator
-// of a 32x32 product leaves in a lane for its first 16 rows.
+constexpr uint32_t row_step(int ks) { return static_cast<uint32_t>(ks) << 5; }
+// Column operand, half i of the first 16 rows: lane l gets, through the
+// transposing read, rows 4 (l / 32) + 8 i .. +3 of column 32 db + l % 32; the
+// two halves give the eight rows that the accumulator of a 32x32 product
+// leaves in a lane for its first 16 rows:  col_base() ^ col_step(db, i).
 template <int D>
-__device__ __forceinline__ uint32_t col_off(int lane, int db, int i) {
-  const uint32_t row = ((lane & 15) >> 2) + 4 * (lane >> 5) + 8 * i;
-  const uint32_t c = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+__device__ __forceinline__ uint32_t col_base(int lane) {
+  const uint32_t row = ((lane & 15) >> 2) + 4 * (lane >> 5);
+  const uint32_t c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   return row * (2 * D) + ((c ^ swz<D>(row)) << 4) + (lane & 1) * 8;
+}
+template <int D>
+constexpr uint32_t col_step(int db, int i) {
+  return (static_cast<uint32_t>(db) << 6) | (static_cast<uint32_t>(i) << 5) |
+         (static_cast<uint32_t>(i) * 16u * D);
 }
 __device__ __forceinline__ u32x4 col_read(const uint8_t* tile, uint32_t off0, uint32_t off1) {
   const u32x2 a = lds_read_tr16(tile + off0), b = lds_read_tr16(tile + off1);
@@ -156,10 +194,17 @@ __device__ __forceinline__ float halves_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// tanh(x) through e = exp(2x): 1 - 2 / (e + 1), which saturates at both ends.
+// tanh(x) to a relative 5e-7: 1 - 2 / (exp(2x) + 1), which saturates at both
+// ends but cancels near 0, where the odd series up to x^9 takes over.
 __device__ __forceinline__ float tanh_f32(float x) {
   const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
-  return __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
+  const float far = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
+  const float y = x * x;
+  float t = __builtin_fmaf(y, 62.0f / 2835.0f, -17.0f / 315.0f);
+  t = __builtin_fmaf(y, t, 2.0f / 15.0f);
+  t = __builtin_fmaf(y, t, -1.0f / 3.0f);
+  const float near = __builtin_fmaf(x * y, t, x);
+  return y < 0.09f ? near : far;
 }
 
 // Eight accumulator values as one operand of eight bf16.
@@ -170,8 +215,8 @@ __device__ __forceinline__ u32x4 pack8(const f32x16& s, int first) {
   return w;
 }
 
-// Where value r of a 32x32 accumulator lies: row 8 (r / 4) + 4 (lane / 32) + r % 4.
-__device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
+// Where value r of a 32x32 accumulator lies: row acc_row(r) + 4 (lane / 32).
+constexpr int acc_row(int r) { return 8 * (r >> 2) + (r & 3); }
 
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;

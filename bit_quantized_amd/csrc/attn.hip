@@ -2,9 +2,9 @@
 //   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i . k_j (capped by a tanh)
 // in one pass over the keys with the running maximum and sum of each query.
 //
-// A workgroup of four waves takes 128 queries of one document and head, a
-// wave 32 of them; key and value tiles of 64 rows go through LDS, the next
-// tile's loads in flight while one is worked on.  The products run as
+// A workgroup of four or eight waves (wide_tiles()) takes 128 or 256 queries
+// of one document and head, a wave 32 of them; key and value tiles of 64 rows
+// go through LDS, the next tile's loads in flight while one is worked on.  The products run as
 // 32x32x16 bf16 matrix instructions on the transposed problem: S^T = K Q^T
 // leaves a query's scores in two lanes (32 apart), so the softmax needs one
 // exchange per tile and its statistics are one value per lane; and the
@@ -20,13 +20,17 @@ using namespace attn_dev;
 
 namespace {
 
-constexpr int BM = 128, BN = 64;
+constexpr int BN = 64;
 
-template <int D, bool CAP>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32;
+// NW waves of 32 queries each.
+template <int D, bool CAP, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
+  constexpr int KS = D / 16, DB = D / 32, BM = 32 * NW;
   constexpr int TB = BN * D * 2;         // bytes of a tile
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TB];   // [buffer][K, V]
+  // (two objects: with one, the compiler waits for all loads in flight before
+  // the transposing reads)
+  __shared__ __attribute__((aligned(16))) uint8_t klds[2 * TB];
+  __shared__ __attribute__((aligned(16))) uint8_t vlds[2 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
@@ -54,9 +58,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
   const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
   const uint32_t lane0 = stage_lane<D>(lane);
   auto fetch = [&](int t) {
-    uint8_t* buf = lds + (t & 1) * 2 * TB;
-    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane, lane0);
-    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane,
+    const int buf = (t & 1) * TB;
+    stage<D, BN, NW>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, klds + buf, wave, lane, lane0);
+    stage<D, BN, NW>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, vlds + buf, wave, lane,
                     lane0);
   };
   fetch(0);
@@ -81,8 +85,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
   staged_barrier();
   for (int t = 0; t < nt; ++t) {
     if (t + 1 < nt) fetch(t + 1);
-    const uint8_t* kt = lds + (t & 1) * 2 * TB;
-    const uint8_t* vt = kt + TB;
+    const uint8_t* kt = klds + (t & 1) * TB;
+    const uint8_t* vt = vlds + (t & 1) * TB;
     f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -163,16 +167,21 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(const AttnArgs a, uint32_t 
   }
 }
 
+template <int D, int NW>
+hipError_t go(const AttnArgs& a, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
+  const dim3 grid(tiles * static_cast<uint32_t>(a.Hq));
+  if (a.softcap > 0) hipLaunchKernelGGL((k_attn_fwd<D, true, NW>), grid, dim3(64 * NW), 0, st, a, tiles);
+  else hipLaunchKernelGGL((k_attn_fwd<D, false, NW>), grid, dim3(64 * NW), 0, st, a, tiles);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st) {
-  const uint32_t tiles = static_cast<uint32_t>(tiles_of<BM>(a));
-  const dim3 grid(tiles * static_cast<uint32_t>(a.Hq));
-#define FT_AF(DD, C) hipLaunchKernelGGL((k_attn_fwd<DD, C>), grid, dim3(256), 0, st, a, tiles)
-  if (D == 128) { if (a.softcap > 0) FT_AF(128, true); else FT_AF(128, false); }
-  else { if (a.softcap > 0) FT_AF(64, true); else FT_AF(64, false); }
-#undef FT_AF
-  return hipGetLastError();
+  const bool wide = wide_tiles(a);
+  if (D == 128) return wide ? go<128, 8>(a, st) : go<128, 4>(a, st);
+  return wide ? go<64, 8>(a, st) : go<64, 4>(a, st);
 }
 
 }  // namespace ft

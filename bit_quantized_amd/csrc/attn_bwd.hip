@@ -23,7 +23,6 @@ using namespace attn_dev;
 
 namespace {
 
-constexpr int BM = 128;
 constexpr int kFewTiles = 4;             // of 64 keys
 
 // A score s to t, with p = exp2(t); `slope` is the cap's derivative there.
@@ -40,9 +39,9 @@ __device__ __forceinline__ float score(float s, float lse2, float c1, float c2, 
   }
 }
 
-template <int D, bool CAP>
-__global__ __launch_bounds__(256, 2) void k_attn_dq(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32, BN = 64;
+template <int D, bool CAP, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32_t tiles) {
+  constexpr int KS = D / 16, DB = D / 32, BN = 64, BM = 32 * NW;
   constexpr int TB = BN * D * 2;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TB];   // [buffer][K, V]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -71,8 +70,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(const AttnArgs a, uint32_t t
   const uint32_t lane0 = stage_lane<D>(lane);
   auto fetch = [&](int t) {
     uint8_t* buf = lds + (t & 1) * 2 * TB;
-    stage<D, BN, 4>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane, lane0);
-    stage<D, BN, 4>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane, lane0);
+    stage<D, BN, NW>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane, lane0);
+    stage<D, BN, NW>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane, lane0);
   };
   fetch(0);
   u32x4 q[KS], g[KS];
@@ -363,24 +362,28 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
   }
 }
 
+template <int D, bool CAP, int NW>
+hipError_t dq_go(const AttnArgs& a, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
+  hipLaunchKernelGGL((k_attn_dq<D, CAP, NW>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0, st, a,
+                     tiles);
+  return hipGetLastError();
+}
+template <int D, bool CAP>
+hipError_t go(const AttnArgs& a, hipStream_t st) {
+  if (hipError_t e = wide_tiles(a) ? dq_go<D, CAP, 8>(a, st) : dq_go<D, CAP, 4>(a, st); e != hipSuccess) return e;
+  constexpr int NW = 4, BQ = 32;
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
+  hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ>), dim3(tiles * static_cast<uint32_t>(a.Hkv)), dim3(64 * NW), 0, st,
+                     a, tiles);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st) {
-  const uint32_t tiles = static_cast<uint32_t>(tiles_of<BM>(a));
-  constexpr int NWK = 4, BQK = 32;
-  const uint32_t ktiles = static_cast<uint32_t>(tiles_of<32 * NWK>(a));
-#define FT_AB(DD, C)                                                                              \
-  do {                                                                                            \
-    hipLaunchKernelGGL((k_attn_dq<DD, C>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(256),  \
-                       0, st, a, tiles);                                                          \
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;                              \
-    hipLaunchKernelGGL((k_attn_dkv<DD, C, NWK, BQK>), dim3(ktiles * static_cast<uint32_t>(a.Hkv)), \
-                       dim3(64 * NWK), 0, st, a, ktiles);                                         \
-  } while (0)
-  if (D == 128) { if (a.softcap > 0) FT_AB(128, true); else FT_AB(128, false); }
-  else { if (a.softcap > 0) FT_AB(64, true); else FT_AB(64, false); }
-#undef FT_AB
-  return hipGetLastError();
+  if (D == 128) return a.softcap > 0 ? go<128, true>(a, st) : go<128, false>(a, st);
+  return a.softcap > 0 ? go<64, true>(a, st) : go<64, false>(a, st);
 }
 
 }  // namespace ft

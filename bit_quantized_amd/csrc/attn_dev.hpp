@@ -99,6 +99,17 @@ inline int64_t tiles_of(const AttnArgs& a) {
   return a.doc ? a.M / BM + a.n_doc + 2 : (a.M + BM - 1) / BM;
 }
 
+// Workgroups of eight waves (256 rows) or of four (128): the registers allow
+// eight waves on a CU either way.  Eight that share the tiles they walk are
+// faster while a CU has all eight (7%: half the loads and barriers), but a
+// last round that would fill at most half of the CUs goes faster as twice
+// as many workgroups of four, and so do problems of less than one round.
+inline bool wide_tiles(const AttnArgs& a) {
+  const int64_t rounds256 = a.M * a.Hq;                  // times 256 rows, 256 CUs
+  const int64_t part = rounds256 % (256 * 256);
+  return rounds256 >= 256 * 256 && (part == 0 || part > 128 * 256);
+}
+
 // A tile of rows in LDS: 2 D bytes a row, its 16-byte chunks permuted by
 // chunk ^ swz(row), so that both ways of reading it are free of bank
 // conflicts: 16 rows of one chunk (ds_read_b128 of a row operand), and 4
@@ -150,8 +161,16 @@ __device__ __forceinline__ void stage(const uint16_t* p, int64_t ld, int have, u
     dma16(r, tile + first * (2 * D), at + static_cast<uint32_t>(first) * row_bytes + (lane0 ^ flip));
   }
 }
+// Wait until at most VM of this wave's loads are in flight (and none of its
+// LDS accesses), then for the workgroup.  (Builtins: the compiler counts the
+// waits, too, and adds none of its own for the loads that are done.)
+template <int VM = 0>
 __device__ __forceinline__ void staged_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((VM & 0xF) | ((VM >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Byte offsets in a tile.  The permutation is an exclusive or, and rows and

@@ -320,7 +320,8 @@ ft_status fourtune_attn_fwd(const ft_attn* d, const uint16_t* q, const uint16_t*
 
 size_t fourtune_attn_workspace_bytes(const ft_attn* d) {
   if (attn_shape(d) != FT_OK) return 0;
-  return align_up(static_cast<size_t>(d->M) * d->Hq * sizeof(float) + 1);
+  return align_up(static_cast<size_t>(d->M) * d->Hq * sizeof(float) + 1) +
+         align_up(ft::attn_part_bytes(d->M, d->Hq, d->Hkv, d->D));
 }
 
 ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do,
@@ -346,6 +347,8 @@ ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.ld_dq = ld_dq; a.ld_dk = ld_dk; a.ld_dv = ld_dv;
   a.delta = static_cast<float*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                    align_up(static_cast<size_t>(d->M) * d->Hq * sizeof(float) + 1));
   hipStream_t st = static_cast<hipStream_t>(stream);
   Timed tm("attn_bwd", st);
   return launched(tm.done(ft::launch_attn_bwd(a, d->D, st)));

@@ -97,9 +97,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint3
     }
     if constexpr (CAP) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < 2; ++kb) {
+        tanh16(s[kb], c1);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[kb][r] = c2 * tanh_f32(s[kb][r] * c1);
+        for (int r = 0; r < 16; ++r) s[kb][r] *= c2;
+      }
     }
     const int last = t * BN + BN - 1;
     if (last >= len || (a.mask != 0 && last > wq0 && last >= dt.prefix)) {

@@ -5,7 +5,7 @@
 //
 // delta_i is also sum_j p_ij dP_ij.  do . o is one pass less but has the
 // rounding of o in it, which shows where a query sees few keys (an o as large
-// as the values); there (up to 256 keys) the sum over the keys is taken.
+// as the values); there (up to 1024 keys) the sum over the keys is taken.
 //
 // Two kernels, so that every sum has one owner and a fixed order (no
 // atomics): k_attn_dq walks the keys of 128 queries and also leaves delta;
@@ -23,21 +23,7 @@ using namespace attn_dev;
 
 namespace {
 
-constexpr int kFewTiles = 4;             // of 64 keys
-
-// A score s to t, with p = exp2(t); `slope` is the cap's derivative there.
-// lse2 = lse / ln 2.
-template <bool CAP>
-__device__ __forceinline__ float score(float s, float lse2, float c1, float c2, float& slope) {
-  if constexpr (CAP) {
-    const float th = tanh_f32(s * c1);
-    slope = __builtin_fmaf(-th, th, 1.0f);
-    return __builtin_fmaf(c2, th, -lse2);
-  } else {
-    slope = 1.0f;
-    return __builtin_fmaf(s, c1, -lse2);
-  }
-}
+constexpr int kFewTiles = 16;            // of 64 keys
 
 template <int D, bool CAP, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32_t tiles) {
@@ -101,8 +87,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
   f32x16 acc[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) acc[db] = zero16();
-  const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
-  const float c2 = a.softcap * kLog2e;
+  // p = exp2(c2 x - lse2) of a score, or of its tanh(c1 x)
+  const float c1 = CAP ? a.scale / a.softcap : 1.0f;
+  const float c2 = (CAP ? a.softcap : a.scale) * kLog2e;
   const int wq0 = q0 + wave * 32;
   int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
   staged_barrier();
@@ -121,10 +108,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
           dp = mfma_bf16_32x32x16(lds_read_b128(kt + TB + at), g[ks], dp);
         }
         const int e = end - t * BN - kb * 32 - 4 * half;
+        if constexpr (CAP) tanh16(s, c1);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          float slope;
-          const float x = score<CAP>(s[r], lse2, c1, c2, slope);
+          const float x = __builtin_fmaf(s[r], c2, -lse2);
           const float p = acc_row(r) < e ? __builtin_amdgcn_exp2f(x) : 0.0f;
           psum += p;
           pdp = __builtin_fmaf(p, dp[r], pdp);
@@ -153,11 +140,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
         s = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + (rbase ^ row_step(ks))), q[ks], s);
         dp = mfma_bf16_32x32x16(lds_read_b128(vt + kb * 32 * 2 * D + (rbase ^ row_step(ks))), g[ks], dp);
       }
+      if constexpr (CAP) tanh16(s, c1);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        float slope;
-        s[r] = score<CAP>(s[r], lse2, c1, c2, slope);
-        dp[r] = CAP ? (dp[r] - delta) * slope : dp[r] - delta;
+        dp[r] -= delta;
+        if constexpr (CAP) dp[r] *= __builtin_fmaf(-s[r], s[r], 1.0f);     // the cap's slope
+        s[r] = __builtin_fmaf(s[r], c2, -lse2);
       }
       if (edge) {
         const int e = end - t * BN - kb * 32 - 4 * half;
@@ -194,7 +182,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
 // 32 NW keys of one key head; a wave owns 32.  Two accumulators of 32 keys by D
 // take half the registers, so V is read from LDS (its rows there stay for the
 // whole walk) and two waves fit on a SIMD.
-template <int D, bool CAP, int NW, int BQ>
+template <int D, bool CAP, int NW, int BQ, bool PART>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint32_t tiles) {
   constexpr int KS = D / 16, DB = D / 32, BM = 32 * NW;
   constexpr int TB = BQ * D * 2;
@@ -204,15 +192,20 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int kvh = static_cast<int>(id / tiles);
+  const int group = a.Hq / a.Hkv;
+  const int kvh = static_cast<int>(id / tiles) / (PART ? group : 1);
+  const int h0 = PART ? static_cast<int>(id / tiles) : kvh * group;       // the first query head
   DocTile dt;
   if (!find_tile<BM>(a, static_cast<int>(id % tiles), dt)) return;
   const int kj = dt.row0 + wave * 32 + l32;              // this lane's key
   const bool live = kj < dt.hi;
   uint16_t* dkrow = a.dk + static_cast<int64_t>(kj) * a.ld_dk + kvh * D;
   uint16_t* dvrow = a.dv + static_cast<int64_t>(kj) * a.ld_dv + kvh * D;
+  float* prow = PART ? a.part + (static_cast<int64_t>(h0) * a.M + kj) * 2 * D : nullptr;
   if (!dt.keys) {
-    if (live) {
+    if (PART) {
+      for (int i = half; live && i < D / 2; i += 2) reinterpret_cast<f32x4*>(prow)[i] = f32x4{0, 0, 0, 0};
+    } else if (live) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         reinterpret_cast<u32x4*>(dkrow)[2 * i + half] = u32x4{0, 0, 0, 0};
@@ -226,8 +219,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
   // the first query that sees a key of the workgroup; whole tiles of 64
   const int first = a.mask == 0 || k0 < dt.prefix ? 0 : k0 / BQ;
   const int nt = (len + BQ - 1) / BQ - first;
-  const int group = a.Hq / a.Hkv;
-  const int total = nt * group;                          // (query head, tile) pairs
+  const int total = PART ? nt : nt * group;              // (query head, tile) pairs
   const uint32_t lane0 = stage_lane<D>(lane);
   auto fetch = [&](int it, int h, int t) {
     uint8_t* buf = lds + (it & 1) * 2 * TB;
@@ -251,7 +243,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
     if (threadIdx.x < 2 * BQ)
       stat[it & 1][threadIdx.x / BQ][threadIdx.x & (BQ - 1)] = threadIdx.x < BQ ? nstat * kLog2e : nstat;
   };
-  int t = first, nh = kvh * group, ntile = first;        // this tile; the next one's head and tile
+  int t = first, nh = h0, ntile = first;        // this tile; the next one's head and tile
   stage<D, BM, NW>(a.v + static_cast<int64_t>(dt.row0) * a.ld_v + kvh * D, a.ld_v, dt.rows, vlds, wave, lane,
                    lane0);
   fetch(0, nh, ntile);
@@ -269,8 +261,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
   f32x16 dk[DB], dv[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
-  const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
-  const float c2 = a.softcap * kLog2e;
+  // p = exp2(c2 x - lse2) of a score, or of its tanh(c1 x)
+  const float c1 = CAP ? a.scale / a.softcap : 1.0f;
+  const float c2 = (CAP ? a.softcap : a.scale) * kLog2e;
   const int wk0 = k0 + wave * 32;                        // the wave's first key
   const bool one_key = len == 1 || (a.mask != 0 && dt.prefix <= 1);        // the first query does
   const int first_seen = wk0 + l32 >= dt.prefix ? wk0 + l32 : 0;   // queries from here on see the key
@@ -305,15 +298,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
                                 lds_read_b128(vl + (rbase ^ row_step(ks))), dp);
       }
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (CAP) tanh16(s, c1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f32x4 lse2 = *reinterpret_cast<const f32x4*>(ls + qb * 32 + 8 * j + 4 * half);
         const f32x4 delta = *reinterpret_cast<const f32x4*>(de + qb * 32 + 8 * j + 4 * half);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float slope;
-          s[4 * j + e] = score<CAP>(s[4 * j + e], lse2[e], c1, c2, slope);
-          dp[4 * j + e] = CAP ? (dp[4 * j + e] - delta[e]) * slope : dp[4 * j + e] - delta[e];
+          const float x = s[4 * j + e];
+          dp[4 * j + e] -= delta[e];
+          if constexpr (CAP) dp[4 * j + e] *= __builtin_fmaf(-x, x, 1.0f);
+          s[4 * j + e] = __builtin_fmaf(x, c2, -lse2[e]);
         }
       }
       if (edge) {
@@ -352,6 +347,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float f = a.scale;
+        if constexpr (PART) {
+          float* at = prow + db * 32 + 8 * i + 4 * half;
+          *reinterpret_cast<f32x4*>(at) = f32x4{dk[db][4 * i] * f, dk[db][4 * i + 1] * f, dk[db][4 * i + 2] * f,
+                                                dk[db][4 * i + 3] * f};
+          *reinterpret_cast<f32x4*>(at + D) = f32x4{dv[db][4 * i], dv[db][4 * i + 1], dv[db][4 * i + 2], dv[db][4 * i + 3]};
+          continue;
+        }
         const u32x2 wk = {cvt_pk_bf16(dk[db][4 * i] * f, dk[db][4 * i + 1] * f),
                           cvt_pk_bf16(dk[db][4 * i + 2] * f, dk[db][4 * i + 3] * f)};
         const u32x2 wv = {cvt_pk_bf16(dv[db][4 * i], dv[db][4 * i + 1]),
@@ -360,6 +362,23 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
         *reinterpret_cast<u32x2*>(dvrow + db * 32 + 8 * i + 4 * half) = wv;
       }
   }
+}
+
+// dK and dV of a row and key head from the sums of its query heads, 4 values
+// a thread.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_dkv_sum(const AttnArgs a) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int c = static_cast<int>(i % (D / 2)) * 4;                        // of [dK, dV]
+  const int64_t rh = i / (D / 2);
+  const int64_t row = rh / a.Hkv;
+  const int kvh = static_cast<int>(rh % a.Hkv), group = a.Hq / a.Hkv;
+  if (row >= a.M) return;
+  f32x4 v = {0, 0, 0, 0};
+  for (int g = 0; g < group; ++g)
+    v += *reinterpret_cast<const f32x4*>(a.part + (static_cast<int64_t>(kvh * group + g) * a.M + row) * 2 * D + c);
+  uint16_t* out = c < D ? a.dk + row * a.ld_dk + kvh * D + c : a.dv + row * a.ld_dv + kvh * D + c - D;
+  *reinterpret_cast<u32x2*>(out) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
 }
 
 template <int D, bool CAP, int NW>
@@ -374,12 +393,25 @@ hipError_t go(const AttnArgs& a, hipStream_t st) {
   if (hipError_t e = wide_tiles(a) ? dq_go<D, CAP, 8>(a, st) : dq_go<D, CAP, 4>(a, st); e != hipSuccess) return e;
   constexpr int NW = 4, BQ = 32;
   const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
-  hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ>), dim3(tiles * static_cast<uint32_t>(a.Hkv)), dim3(64 * NW), 0, st,
-                     a, tiles);
+  if (attn_split_heads(a.M, a.Hq, a.Hkv)) {
+    hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ, true>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW),
+                       0, st, a, tiles);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_attn_dkv_sum<D>, dim3(static_cast<uint32_t>((a.M * a.Hkv * (D / 2) + 255) / 256)), dim3(256),
+                       0, st, a);
+  } else {
+    hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ, false>), dim3(tiles * static_cast<uint32_t>(a.Hkv)), dim3(64 * NW),
+                       0, st, a, tiles);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
+
+bool attn_split_heads(int64_t M, int Hq, int Hkv) { return Hq > Hkv && M * Hkv < int64_t(512) * 128; }
+size_t attn_part_bytes(int64_t M, int Hq, int Hkv, int D) {
+  return attn_split_heads(M, Hq, Hkv) ? static_cast<size_t>(M) * Hq * 2 * D * sizeof(float) : 0;
+}
 
 hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st) {
   if (D == 128) return a.softcap > 0 ? go<128, true>(a, st) : go<128, false>(a, st);

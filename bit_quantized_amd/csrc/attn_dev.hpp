@@ -213,17 +213,35 @@ __device__ __forceinline__ float halves_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// tanh(x) to a relative 5e-7: 1 - 2 / (exp(2x) + 1), which saturates at both
-// ends but cancels near 0, where the odd series up to x^9 takes over.
-__device__ __forceinline__ float tanh_f32(float x) {
-  const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
-  const float far = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
-  const float y = x * x;
+// tanh of c x for a whole accumulator, to a relative 5e-7: the odd series up
+// to x^9 where |c x| < 0.3, else 1 - 2 / (exp(2 c x) + 1), which saturates at
+// both ends but cancels near 0.  A cap is usually far above the scores, so
+// the wave looks first whether all of them are in the series' range.
+__device__ __forceinline__ float tanh_near(float x, float y) {
   float t = __builtin_fmaf(y, 62.0f / 2835.0f, -17.0f / 315.0f);
   t = __builtin_fmaf(y, t, 2.0f / 15.0f);
   t = __builtin_fmaf(y, t, -1.0f / 3.0f);
-  const float near = __builtin_fmaf(x * y, t, x);
-  return y < 0.09f ? near : far;
+  return __builtin_fmaf(x * y, t, x);
+}
+__device__ __forceinline__ void tanh16(f32x16& s, float c) {
+  float most = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    s[r] *= c;
+    most = fmaxf(most, __builtin_fabsf(s[r]));
+  }
+  if (__any(!(most < 0.3f))) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const float x = s[r], y = x * x;
+      const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
+      const float far = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
+      s[r] = y < 0.09f ? tanh_near(x, y) : far;
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = tanh_near(s[r], s[r] * s[r]);
+  }
 }
 
 // Eight accumulator values as one operand of eight bf16.

@@ -290,7 +290,12 @@ struct AttnArgs {
   uint16_t *dq, *dk, *dv;
   int64_t ld_dq, ld_dk, ld_dv;
   float* delta;                   // [Hq, M]
+  float* part;                    // [Hq, M, 2, D] with attn_split_heads
 };
+// The query heads of a key head are divided between workgroups where whole
+// key heads would be fewer than 512 of them.
+bool attn_split_heads(int64_t M, int Hq, int Hkv);
+size_t attn_part_bytes(int64_t M, int Hq, int Hkv, int D);
 hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st);
 

@@ -222,13 +222,13 @@ __global__ __launch_bounds__(kMaxWaves * 64) void k_norm_bwd(const NormArgs a) {
 }
 
 // The sums of each sample's slots and of all samples: one workgroup per 64
-// columns and sample (index n_seg: the weights' gradients), 16 threads a
-// column, whose partial sums are added in order.
-constexpr int kCols = 64, kWays = 16;
-__global__ __launch_bounds__(kCols* kWays) void k_norm_reduce(const NormArgs a) {
-  __shared__ float acc[kWays][kCols];
-  const int c = static_cast<int>(blockIdx.x) * kCols + (threadIdx.x & (kCols - 1));
-  const int way = threadIdx.x / kCols;
+// columns and sample (index n_seg: the weights' gradients), 32 threads for
+// four columns, whose partial sums are added in order.
+constexpr int kQuads = 16, kWays = 32;
+__global__ __launch_bounds__(kQuads* kWays) void k_norm_reduce(const NormArgs a) {
+  __shared__ f32x4 acc[kWays][kQuads];
+  const int quad = threadIdx.x % kQuads, way = threadIdx.x / kQuads;
+  const int c = (static_cast<int>(blockIdx.x) * kQuads + quad) * 4;
   const int b = static_cast<int>(blockIdx.y);
   const bool in = c < a.C;
   const int kind = static_cast<int>(blockIdx.z);     // 0: A1, 1: A2, 2: A3
@@ -236,41 +236,50 @@ __global__ __launch_bounds__(kCols* kWays) void k_norm_reduce(const NormArgs a) 
                           : (kind == 0 ? a.dweight : kind == 2 ? a.dpost_weight : nullptr);
   if (!out) return;
   auto sum = [&](int s) {
-    float v = 0.0f;
+    f32x4 v = {0, 0, 0, 0};
     const int r0 = sample_first(a, s), r1 = sample_first(a, s + 1);
     if (r1 <= r0 || !in) return v;
     const int g1 = (r1 - 1) / a.rows_per_wg;
     const float* p = a.part + kind * a.C + c;
+#pragma unroll 8
     for (int g = r0 / a.rows_per_wg + way; g <= g1; g += kWays)
-      v += p[static_cast<int64_t>(g + s) * 3 * a.C];
+      v += *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(g + s) * 3 * a.C);
     return v;
   };
   auto ld = [&](const uint16_t* p, int64_t i, float none) { return p ? bf16_to_f32(p[i]) : none; };
-  float v = 0.0f;
+  f32x4 v = {0, 0, 0, 0};
   if (b < a.n_seg) {
     v = sum(b);
   } else {
     for (int s = 0; s < a.n_seg; ++s) {
-      const float f = !in ? 0.0f
-                      : kind == 0 ? 1.0f + ld(a.scale, s * a.ld_mod + c, 0.0f)
-                                  : a.alpha * ld(a.gate, s * a.ld_mod + c, 1.0f);
-      v = __builtin_fmaf(f, sum(s), v);
+      const f32x4 t = sum(s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = !in ? 0.0f
+                        : kind == 0 ? 1.0f + ld(a.scale, s * a.ld_mod + c + e, 0.0f)
+                                    : a.alpha * ld(a.gate, s * a.ld_mod + c + e, 1.0f);
+        v[e] = __builtin_fmaf(f, t[e], v[e]);
+      }
     }
   }
-  acc[way][threadIdx.x & (kCols - 1)] = v;
+  acc[way][quad] = v;
   __syncthreads();
-  if (way != 0 || !in) return;
-  v = acc[0][threadIdx.x];
+  // one value a thread
+  if (threadIdx.x >= kQuads * 4) return;
+  const int q = threadIdx.x / 4, e = threadIdx.x % 4;
+  const int col = (static_cast<int>(blockIdx.x) * kQuads + q) * 4 + e;
+  if (col >= a.C) return;
+  float t = acc[0][q][e];
 #pragma unroll
-  for (int i = 1; i < kWays; ++i) v += acc[i][threadIdx.x];
-  int64_t o = c;
+  for (int i = 1; i < kWays; ++i) t += acc[i][q][e];
+  int64_t o = col;
   if (b < a.n_seg) {
     o += b * a.ld_dmod;
-    if (kind == 0) v *= ld(a.weight, c, 1.0f);
-    if (kind == 2) v *= a.alpha * ld(a.post_weight, c, 1.0f);
+    if (kind == 0) t *= ld(a.weight, col, 1.0f);
+    if (kind == 2) t *= a.alpha * ld(a.post_weight, col, 1.0f);
   }
-  if (a.grad_f32) static_cast<float*>(out)[o] = v;
-  else static_cast<uint16_t*>(out)[o] = static_cast<uint16_t>(cvt_pk_bf16(v, 0.0f));
+  if (a.grad_f32) static_cast<float*>(out)[o] = t;
+  else static_cast<uint16_t*>(out)[o] = static_cast<uint16_t>(cvt_pk_bf16(t, 0.0f));
 }
 
 // Vectors of a lane (1, 2 or 4) and waves of a workgroup.
@@ -320,9 +329,9 @@ hipError_t launch_norm_bwd(const NormArgs& in, hipStream_t st) {
     e = v == 1 ? go<1>(a, st) : v == 2 ? go<2>(a, st) : go<4>(a, st);
   }
   if (e != hipSuccess || !a.part) return e;
-  const dim3 grid(static_cast<uint32_t>((a.C + kCols - 1) / kCols),
+  const dim3 grid(static_cast<uint32_t>((a.C + 4 * kQuads - 1) / (4 * kQuads)),
                   static_cast<uint32_t>(a.n_seg + (a.dweight || a.dpost_weight ? 1 : 0)), 3);
-  hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kCols * kWays), 0, st, a);
+  hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kQuads * kWays), 0, st, a);
   return hipGetLastError();
 }
 

@@ -5,13 +5,16 @@
 //             dx = rstd (w u - n mean(w u n)),  n = x rstd
 //
 // Memory bound: every head is read and written once.  A head is D / 8 lanes
-// with eight values each (16-byte loads), rounded up to a power of two, so a
-// wave holds 64 / LPH heads of one row, and a lane's pairs are the same for
-// every head of the row: their sines and cosines are computed once per row,
-// from the position and the table of frequencies in the launch's arguments
-// (no table in memory to read).  The angle is taken in turns, p * (hi + lo)
-// with the fraction of p * hi exact, because the hardware's sine and cosine
-// take turns; at position 2^24 the angle is still good to 2^-20 of a turn.
+// with eight values each, rounded up to a power of two, so a wave holds
+// 64 / LPH heads of one row, and a lane's pairs are the same for every head
+// of the row: their sines and cosines are computed once per row, from the
+// position and the table of frequencies in the launch's arguments (no table
+// in memory to read), while the first heads are on their way.  A lane's
+// eight values are four whole pairs in either layout: one 16-byte piece, or
+// two of 8 bytes a half apart, so no lane needs another's values but for the
+// norm's sum.  The angle is taken in turns, p * (hi + lo) with the fraction of
+// p * hi exact, because the hardware's sine and cosine take turns; at
+// position 2^24 the angle is still good to 2^-20 of a turn.
 #include <algorithm>
 
 #include "norm_dev.hpp"
@@ -24,7 +27,7 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// sin and cos of position p times the frequency of pair j.
+// sin and cos of position p times the frequency hi + lo (turns).
 __device__ __forceinline__ void turn(float p, float hi, float lo, float& s, float& c) {
   const float r = p * hi;
   const float e = __builtin_fmaf(p, hi, -r);
@@ -33,76 +36,80 @@ __device__ __forceinline__ void turn(float p, float hi, float lo, float& s, floa
   c = __builtin_amdgcn_cosf(f);
 }
 
-// LPH lanes per head; HALVES: pair j is (j, j + n_pairs), whose partner
-// vector sits n_pairs / 8 lanes away; BWD: the transposed rotation, and
-// the norm's gradient.  DW: the weights' gradients too.
+// Eight values of a head: at a0 .. +7 (PAIRS), or at a0 .. +3 and a1 .. +3.
+template <bool HALVES>
+__device__ __forceinline__ Raw8<0> load8(const uint16_t* p, int a0, int a1) {
+  Raw8<0> v;
+  if constexpr (HALVES) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p + a0), y = *reinterpret_cast<const u32x2*>(p + a1);
+    v.w = u32x4{x[0], x[1], y[0], y[1]};
+  } else {
+    v.w = *reinterpret_cast<const u32x4*>(p + a0);
+  }
+  return v;
+}
+template <bool HALVES>
+__device__ __forceinline__ void store8(uint16_t* p, int a0, int a1, const Raw8<0>& v) {
+  if constexpr (HALVES) {
+    *reinterpret_cast<u32x2*>(p + a0) = u32x2{v.w[0], v.w[1]};
+    *reinterpret_cast<u32x2*>(p + a1) = u32x2{v.w[2], v.w[3]};
+  } else {
+    *reinterpret_cast<u32x4*>(p + a0) = v.w;
+  }
+}
+
+// LPH lanes per head.  BWD: the transposed rotation, and the norm's gradient.
 template <int LPH, bool HALVES, bool BWD>
 __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows_per_wave,
                                                        int head_splits) {
   constexpr int HPW = 64 / LPH;          // heads of a wave
-  constexpr int NP = HALVES ? 8 : 4;     // pairs a lane's vector meets
-  constexpr int UN = 4;                  // heads in flight per lane
+  constexpr int UN = 2;                  // heads in flight per lane (3 and 4: fewer waves, slower)
   __shared__ float dwl[BWD ? kWaves * 2 * LPH * 8 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int vec = lane % LPH, hsub = lane / LPH;
   const int D = a.t.D, np = a.t.n_pairs;
   const bool in_head = vec * 8 < D;
-  // the lane's pairs, their axes and frequencies
-  const int hv = np >> 3;                // HALVES: vectors of a half
-  const bool second = HALVES && vec >= hv;
-  const bool turned = vec * 8 < 2 * np;
-  const int partner = second ? lane - hv : lane + hv;
-  float hi[NP], lo[NP];
-  int ax[NP];
+  const bool turned = vec * 4 < np;      // the lane's four pairs (the last lane's may be fewer)
+  // where the lane's values lie; those past the pairs are eight in a row
+  const int a0 = !HALVES ? 8 * vec : turned ? 4 * vec : 8 * vec;
+  const int a1 = turned ? np + 4 * vec : 8 * vec + 4;
+  float dw[2][8];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int j = HALVES ? (second ? vec - hv : vec) * 8 + i : vec * 4 + i;
-    const bool has = turned && j < np;
+  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.0f;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  float hi[4], lo[4];
+  int ax[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = vec * 4 + i;
+    const bool has = j < np;
     hi[i] = has ? a.t.turn_hi[has ? j : 0] : 0.0f;
     lo[i] = has ? a.t.turn_lo[has ? j : 0] : 0.0f;
     ax[i] = has ? a.t.axis[has ? j : 0] : 0;
   }
-  const float inv_d = 1.0f / static_cast<float>(D);
-  float dw[2][8];
+  Raw8<0> wt[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.0f;
+  for (int si = 0; si < 2; ++si) {
+    wt[si].w = u32x4{kOnes, kOnes, kOnes, kOnes};
+    if (a.side[si].weight && in_head) wt[si] = load8<HALVES>(a.side[si].weight, a0, a1);
+  }
+  const int step = HPW * head_splits;
 
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * rows_per_wave;
   const int64_t row1 = min(row0 + rows_per_wave, a.M);
   for (int64_t row = row0; row < row1; ++row) {
-    float sn[NP], cs[NP];
+    int pos[4];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const float p = static_cast<float>(a.pos[row * a.t.n_axes + ax[i]]);
-      turn(p, hi[i], lo[i], sn[i], cs[i]);
-      if (BWD) sn[i] = -sn[i];
-      if (HALVES && !second) sn[i] = -sn[i];   // out_a = t_a cos - t_b sin, out_b = t_b cos + t_a sin
-    }
-    // the rotation of a lane's eight values
-    auto rotate = [&](float(&t)[8]) {
-      if constexpr (HALVES) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl(t[e], partner);
-          t[e] = turned ? __builtin_fmaf(o, sn[e], t[e] * cs[e]) : t[e];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = t[2 * i], y = t[2 * i + 1];
-          t[2 * i] = x * cs[i] - y * sn[i];
-          t[2 * i + 1] = __builtin_fmaf(x, sn[i], y * cs[i]);
-        }
-      }
-    };
+    for (int i = 0; i < 4; ++i) pos[i] = a.pos[row * a.t.n_axes + ax[i]];
+    float sn[4], cs[4];
+    bool have = false;
 #pragma unroll
     for (int si = 0; si < 2; ++si) {
       const RopeSide& s = a.side[si];
       const bool norm = s.weight != nullptr;
-      Raw8<0> wr;
-      wr.w = u32x4{kOnes, kOnes, kOnes, kOnes};
-      if (norm && in_head) wr.load(s.weight, vec);
-      const int step = HPW * head_splits;
+      const uint16_t* in = s.in + row * s.ld_in;
+      const uint16_t* xin = s.x + row * s.ld_x;
+      uint16_t* outp = s.out + row * s.ld_out;
       for (int h0 = static_cast<int>(blockIdx.y) * HPW; h0 < s.heads; h0 += step * UN) {
         Raw8<0> v[UN], xv[UN];
         bool ok[UN];
@@ -113,10 +120,28 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows
           v[u].zero();
           xv[u].zero();
           if (ok[u]) {
-            v[u].load(s.in + row * s.ld_in + static_cast<int64_t>(h) * D, vec);
-            if (BWD && norm) xv[u].load(s.x + row * s.ld_x + static_cast<int64_t>(h) * D, vec);
+            v[u] = load8<HALVES>(in + static_cast<int64_t>(h) * D, a0, a1);
+            if (BWD && norm) xv[u] = load8<HALVES>(xin + static_cast<int64_t>(h) * D, a0, a1);
           }
         }
+        if (!have) {
+          have = true;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            turn(static_cast<float>(pos[i]), hi[i], lo[i], sn[i], cs[i]);
+            if (BWD) sn[i] = -sn[i];
+          }
+        }
+        // the rotation of a lane's four pairs
+        auto rotate = [&](float(&t)[8]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int p = HALVES ? i : 2 * i, q = HALVES ? i + 4 : 2 * i + 1;
+            const float x = t[p], y = t[q];
+            t[p] = x * cs[i] - y * sn[i];
+            t[q] = __builtin_fmaf(x, sn[i], y * cs[i]);
+          }
+        };
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
           if (h0 + u * step >= s.heads) break;       // uniform
@@ -130,7 +155,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows
               for (int e = 0; e < 8; ++e) q = __builtin_fmaf(t[e], t[e], q);
               const float rstd = 1.0f / __builtin_sqrtf(lanes_sum<LPH>(q) * inv_d + a.eps);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) t[e] = t[e] * rstd * wr.get(e);
+              for (int e = 0; e < 8; ++e) t[e] = t[e] * rstd * wt[si].get(e);
             }
             rotate(t);
           } else {
@@ -145,7 +170,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows
               for (int e = 0; e < 8; ++e) {
                 const float n = xv[u].get(e) * rstd;
                 dw[si][e] = __builtin_fmaf(t[e], n, dw[si][e]);
-                t[e] *= wr.get(e);
+                t[e] *= wt[si].get(e);
                 m = __builtin_fmaf(t[e], n, m);
               }
               m = lanes_sum<LPH>(m) * inv_d;
@@ -156,7 +181,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows
           if (ok[u]) {
             Raw8<0> o;
             o.set(t);
-            o.store(s.out + row * s.ld_out + static_cast<int64_t>(h0 + u * step + hsub) * D, vec);
+            store8<HALVES>(outp + static_cast<int64_t>(h0 + u * step + hsub) * D, a0, a1, o);
           }
         }
       }
@@ -172,7 +197,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows
         float v = dw[si][e];
 #pragma unroll
         for (int k = LPH; k < 64; k *= 2) v += __shfl_xor(v, k);
-        if (hsub == 0) dwl[(wave * 2 + si) * LPH * 8 + vec * 8 + e] = v;
+        const int at = HALVES ? (e < 4 ? a0 + e : a1 + e - 4) : a0 + e;
+        if (hsub == 0 && in_head) dwl[(wave * 2 + si) * LPH * 8 + at] = v;
       }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kWaves * 64) {
@@ -185,30 +211,34 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope(const RopeArgs a, int rows
   }
 }
 
-// The weights' gradients: the workgroups' sums added in order, 16 threads a value.
-constexpr int kCols = 16, kWays = 16;
-__global__ __launch_bounds__(kCols* kWays) void k_rope_reduce(const RopeArgs a, int n) {
-  __shared__ float acc[kWays][kCols];
+// The weights' gradients: the workgroups' sums added in a fixed order, 64
+// threads for four values.
+constexpr int kQuads = 4, kWays = 64;
+__global__ __launch_bounds__(kQuads* kWays) void k_rope_reduce(const RopeArgs a, int n) {
+  __shared__ f32x4 acc[kWays][kQuads];
   const int D = a.t.D;
-  const int col = threadIdx.x % kCols, way = threadIdx.x / kCols;
-  const int i = static_cast<int>(blockIdx.x) * kCols + col;      // 2 D is a multiple of 16
-  float v = 0.0f;
-  for (int g = way; g < n; g += kWays) v += a.part[static_cast<int64_t>(g) * 2 * D + i];
-  acc[way][col] = v;
+  const int quad = threadIdx.x % kQuads, way = threadIdx.x / kQuads;
+  const int i = (static_cast<int>(blockIdx.x) * kQuads + quad) * 4;      // 2 D is a multiple of 16
+  f32x4 v = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int g = way; g < n; g += kWays)
+    v += *reinterpret_cast<const f32x4*>(a.part + static_cast<int64_t>(g) * 2 * D + i);
+  acc[way][quad] = v;
   __syncthreads();
-  if (way != 0) return;
-  v = acc[0][col];
-#pragma unroll
-  for (int w = 1; w < kWays; ++w) v += acc[w][col];
-  void* out = a.side[i / D].dweight;
+  if (threadIdx.x >= kQuads * 4) return;
+  const int q = threadIdx.x / 4, e = threadIdx.x % 4;                    // one value each
+  float s = 0.0f;
+  for (int w = 0; w < kWays; ++w) s += acc[w][q][e];
+  const int at = (static_cast<int>(blockIdx.x) * kQuads + q) * 4 + e;
+  void* out = a.side[at / D].dweight;
   if (!out) return;
-  if (a.grad_f32) static_cast<float*>(out)[i % D] = v;
-  else static_cast<uint16_t*>(out)[i % D] = static_cast<uint16_t>(cvt_pk_bf16(v, 0.0f));
+  if (a.grad_f32) static_cast<float*>(out)[at % D] = s;
+  else static_cast<uint16_t*>(out)[at % D] = static_cast<uint16_t>(cvt_pk_bf16(s, 0.0f));
 }
 
-// With weight gradients a wave walks several rows, so that at most 512
+// With weight gradients a wave walks several rows, so that at most 1024
 // workgroups leave partial sums.
-constexpr int64_t kMaxPart = 512;
+constexpr int64_t kMaxPart = 1024;
 int rows_per_wave(int64_t M, bool part) {
   return part ? static_cast<int>((M + kMaxPart * kWaves - 1) / (kMaxPart * kWaves)) : 1;
 }
@@ -230,7 +260,7 @@ hipError_t go(const RopeArgs& a, bool bwd, hipStream_t st) {
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   if (!a.part) return hipSuccess;
-  hipLaunchKernelGGL(k_rope_reduce, dim3(2 * a.t.D / kCols), dim3(kCols * kWays), 0, st, a,
+  hipLaunchKernelGGL(k_rope_reduce, dim3(2 * a.t.D / (4 * kQuads)), dim3(kQuads * kWays), 0, st, a,
                      static_cast<int>(wgs));
   return hipGetLastError();
 }

@@ -11,8 +11,6 @@ calls the library.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import ops
@@ -22,49 +20,46 @@ _MASKS = {"full": ops.FT_MASK_FULL, "causal": ops.FT_MASK_CAUSAL, "prefix": ops.
 _LAYOUTS = {"pairs": ops.FT_ROPE_PAIRS, "halves": ops.FT_ROPE_HALVES}
 _LADDERS = {"axis": ops.FT_ROPE_AXIS, "shared": ops.FT_ROPE_SHARED}
 _STATES = {"f32": ops.FT_STATE_F32, "q8": ops.FT_STATE_Q8}
-_DTYPES = {torch.bfloat16: ops.FT_BF16, torch.float32: ops.FT_F32}
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_DTYPES = {_BF16: ops.FT_BF16, _F32: ops.FT_F32}
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{what} must be bfloat16 or float32, not {t.dtype}")
-    return _DTYPES[t.dtype]
-
-
-def _is(t, dtype, what):
-    if t is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-
-
-def _shape(t, shape, what):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+def _on(stream):
+    """Work on another stream than the current one: outputs and workspaces are
+    allocated for the stream that uses them."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _rows(t, shape, dtype, what):
     """A contiguous tensor of that shape and type, or None."""
-    _is(t, dtype, what)
-    _shape(t, shape, what)
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"{what} must be contiguous and of the shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _head_ld(t: torch.Tensor, heads, dim, what: str) -> int:
-    """Row stride of a [M, heads, dim] tensor whose rows hold their heads in one piece."""
-    _is(t, torch.bfloat16, what)
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{what} must be [M, {'heads' if heads is None else heads}, {dim}], not {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+def _heads(t, M, heads, dim, what: str) -> int:
+    """Row stride of a bf16 [M, heads, dim] tensor whose rows hold their heads in one piece."""
+    if t.dtype is not _BF16:
+        raise TypeError(f"{what} must be {_BF16}, not {t.dtype}")
+    if t.shape != (M, heads, dim):
+        raise ValueError(f"{what} must be {(M, heads, dim)}, not {tuple(t.shape)}")
+    ld, step, one = t.stride()
+    if (one != 1 or (step != dim and heads > 1)) and t.numel():
         raise ValueError(f"the heads of a row of {what} must lie next to each other")
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), t.shape[1] * dim)
+    return ld if M > 1 else max(ld, heads * dim)
 
 
 def _offsets(t, what):
-    if t is not None:
-        _is(t, torch.int32, what)
-        if t.dim() != 1 or t.numel() < 2 or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous vector of at least two row offsets")
-    return 1 if t is None else int(t.numel()) - 1
+    """How many ranges a vector of row offsets cuts."""
+    if t is None:
+        return 1
+    if t.dtype is not _I32:
+        raise TypeError(f"{what} must be {_I32}, not {t.dtype}")
+    if t.dim() != 1 or t.shape[0] < 2 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of at least two row offsets")
+    return t.shape[0] - 1
 
 
 class GatedNorm:
@@ -81,70 +76,87 @@ class GatedNorm:
                  eps: float = 1e-6, alpha: float = 1.0):
         self.norm, self.post_norm = _NORMS[norm], _NORMS[post_norm]
         self.weight, self.post_weight = weight, post_weight
-        _is(weight, torch.bfloat16, "weight")
-        _is(post_weight, torch.bfloat16, "post_weight")
         self.eps, self.alpha = float(eps), float(alpha)
-        self._ws = None
 
     def desc(self, x: torch.Tensor, gate=None, scale=None, shift=None, segments=None) -> ops.FtNorm:
-        if x.dim() != 2 or not x.is_contiguous():
-            raise ValueError("x must be a contiguous [M, C] tensor")
+        if x.dim() != 2 or x.dtype not in _DTYPES or not x.is_contiguous():
+            raise ValueError("x must be a contiguous [M, C] tensor in bfloat16 or float32")
         M, C = x.shape
-        mods = [t for t in (gate, scale, shift) if t is not None]
-        n_seg = _offsets(segments, "segments") if segments is not None else (mods[0].shape[0] if mods else 1)
-        ld = C
-        for t in mods:
-            _is(t, torch.bfloat16, "a modulation")
-            _shape(t, (n_seg, C), "a modulation")
-            if t.stride(1) != 1:
-                raise ValueError("a modulation's channels must lie next to each other")
-        if mods and n_seg > 1:
-            ld = int(mods[0].stride(0))
-            if any(t.stride(0) != ld for t in mods):
-                raise ValueError("gate, scale and shift must have one row stride")
-        for t, what in ((self.weight, "weight"), (self.post_weight, "post_weight")):
-            _shape(t, (C,), what)
+        n_seg, ld = (None if segments is None else _offsets(segments, "segments")), None
+        for t, what in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+            if t is None:
+                continue
+            if n_seg is None:
+                n_seg = t.shape[0]
+            if t.dtype is not _BF16 or t.shape != (n_seg, C):
+                raise ValueError(f"{what} must be a bfloat16 {(n_seg, C)} tensor, not {t.dtype} {tuple(t.shape)}")
+            row, one = t.stride()
+            if n_seg == 1:
+                row = C
+            if one != 1 or (ld is not None and row != ld):
+                raise ValueError("gate, scale and shift must have their channels in one piece and one row stride")
+            ld = row
+        w, pw = self.weight, self.post_weight
+        _rows(w, (C,), _BF16, "weight")
+        _rows(pw, (C,), _BF16, "post_weight")
         p = ops._ptr
-        return ops.FtNorm(M, C, n_seg, _dtype(x, "x"), p(segments), self.norm, self.post_norm, self.eps,
-                          self.alpha, p(self.weight), p(self.post_weight), p(scale), p(shift), p(gate), ld)
+        return ops.FtNorm(M, C, n_seg or 1, _DTYPES[x.dtype], p(segments), self.norm, self.post_norm, self.eps,
+                          self.alpha, p(w), p(pw), p(scale), p(shift), p(gate), C if ld is None else ld)
 
     def forward(self, x, y=None, gate=None, scale=None, shift=None, segments=None, need_h: bool = True,
                 stream=None):
         """(r, h, stats); r is x itself without y, h None without need_h."""
-        d = self.desc(x, gate, scale, shift, segments)
-        _rows(y, x.shape, torch.bfloat16, "y")
+        if stream is not None:
+            with _on(stream):
+                return self.forward(x, y, gate, scale, shift, segments, need_h)
         if y is None and not need_h:
             return x, None, None
-        r = x if y is None else torch.empty_like(x)
-        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if need_h else None
-        stats = torch.empty((x.shape[0], 4), dtype=torch.float32, device=x.device)
-        ops.fourtune_norm_fwd(d, x, y, None if y is None else r, h, stats, stream)
-        return r, h, stats
+        d = self.desc(x, gate, scale, shift, segments)
+        _rows(y, x.shape, _BF16, "y")
+        r = None if y is None else torch.empty_like(x)
+        h = x.new_empty(x.shape, dtype=_BF16) if need_h else None
+        stats = x.new_empty((d.M, 4), dtype=_F32)
+        ops.fourtune_norm_fwd(d, x, y, r, h, stats)
+        return x if r is None else r, h, stats
 
     def backward(self, dh, dr, r, y, stats, gate=None, scale=None, shift=None, segments=None,
                  need_weights: bool = True, grad_f32: bool = False, stream=None) -> dict:
         """Gradients by name: dx, dy, dscale, dshift, dgate, dweight,
         dpost_weight; None where there is nothing to differentiate."""
+        if stream is not None:
+            with _on(stream):
+                return self.backward(dh, dr, r, y, stats, gate, scale, shift, segments, need_weights, grad_f32)
         d = self.desc(r, gate, scale, shift, segments)
-        M, C = r.shape
-        dev, low = r.device, torch.bfloat16
-        _rows(dh, r.shape, low, "dh")
-        _rows(dr, r.shape, r.dtype, "dr")
-        _rows(y, r.shape, low, "y")
-        _rows(stats, (M, 4), torch.float32, "stats")
-        gdt = torch.float32 if grad_f32 else low
-        mod = lambda t, has: torch.empty((d.n_seg, C), dtype=gdt, device=dev) if t is not None and has else None
-        vec = lambda t, has: torch.empty((C,), dtype=gdt, device=dev) if t is not None and has and need_weights else None
-        has_h, has_y = dh is not None, y is not None
-        g = dict(dx=torch.empty_like(r), dy=torch.empty_like(y) if has_y else None,
-                 dscale=mod(scale, has_h), dshift=mod(shift, has_h), dgate=mod(gate, has_y),
-                 dweight=vec(self.weight, has_h), dpost_weight=vec(self.post_weight, has_y))
-        ws = None
-        if any(g[k] is not None for k in ("dscale", "dshift", "dgate", "dweight", "dpost_weight")):
-            ws = torch.empty((ops.fourtune_norm_workspace_bytes(d),), dtype=torch.uint8, device=dev)
-        ops.fourtune_norm_bwd(d, dh, dr, r, y, stats, g["dx"], g["dy"], g["dscale"], g["dshift"], g["dgate"], C,
-                              g["dweight"], g["dpost_weight"], ops.FT_F32 if grad_f32 else ops.FT_BF16, ws,
-                              0 if ws is None else ws.numel(), stream)
+        shape, C = r.shape, d.C
+        _rows(dh, shape, _BF16, "dh")
+        _rows(dr, shape, r.dtype, "dr")
+        _rows(y, shape, _BF16, "y")
+        _rows(stats, (d.M, 4), _F32, "stats")
+        gdt = _F32 if grad_f32 else _BF16
+        mods = (d.n_seg, C)
+        new = r.new_empty
+        g = dict(dx=torch.empty_like(r), dy=None, dscale=None, dshift=None, dgate=None, dweight=None,
+                 dpost_weight=None)
+        if dh is not None:
+            if scale is not None:
+                g["dscale"] = new(mods, dtype=gdt)
+            if shift is not None:
+                g["dshift"] = new(mods, dtype=gdt)
+            if need_weights and self.weight is not None:
+                g["dweight"] = new((C,), dtype=gdt)
+        if y is not None:
+            g["dy"] = torch.empty_like(y)
+            if gate is not None:
+                g["dgate"] = new(mods, dtype=gdt)
+            if need_weights and self.post_weight is not None:
+                g["dpost_weight"] = new((C,), dtype=gdt)
+        dx, dy, *sums = g.values()
+        ws, size = None, 0
+        if any(t is not None for t in sums):
+            size = ops.fourtune_norm_workspace_bytes(d)
+            ws = new((size,), dtype=_U8)
+        ops.fourtune_norm_bwd(d, dh, dr, r, y, stats, dx, dy, *sums[:3], C, *sums[3:],
+                              ops.FT_F32 if grad_f32 else ops.FT_BF16, ws, size)
         return g
 
 
@@ -164,25 +176,26 @@ class AxialRotary:
         self.n_axes = len(axis_dims)
         self.q_weight, self.k_weight = q_weight, k_weight
         for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            _rows(t, (self.D,), torch.bfloat16, what)
+            _rows(t, (self.D,), _BF16, what)
 
-    def _side(self, t, out, weight, what):
-        return ops.rope_side(t.shape[1], t, out, _head_ld(t, None, self.D, what),
-                             _head_ld(out, t.shape[1], self.D, what + "'s output"), weight)
+    def _side(self, t, out, M, weight, what):
+        heads = t.shape[1]
+        return ops.rope_side(heads, t, out, _heads(t, M, heads, self.D, what), _heads(out, M, heads, self.D, what), weight)
 
     def forward(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """(q', k'), new [M, heads, D] tensors unless given (which may be q and k
         themselves).  positions: int32 [M, axes]."""
-        M = int(q.shape[0])
-        _rows(positions, (M, self.n_axes), torch.int32, "positions")
-        if k.shape[0] != M:
-            raise ValueError("q and k must have the same rows")
-        new = lambda t, o: torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) if o is None else o
-        q_out, k_out = new(q, q_out), new(k, k_out)
-        _shape(q_out, q.shape, "q_out")
-        _shape(k_out, k.shape, "k_out")
-        ops.fourtune_rope_fwd(self.table, M, positions, self.eps, self._side(q, q_out, self.q_weight, "q"),
-                              self._side(k, k_out, self.k_weight, "k"), stream)
+        if stream is not None:
+            with _on(stream):
+                return self.forward(q, k, positions, q_out, k_out)
+        M = q.shape[0]
+        _rows(positions, (M, self.n_axes), _I32, "positions")
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        if k_out is None:
+            k_out = k.new_empty(k.shape)
+        ops.fourtune_rope_fwd(self.table, M, positions, self.eps, self._side(q, q_out, M, self.q_weight, "q"),
+                              self._side(k, k_out, M, self.k_weight, "k"))
         return q_out, k_out
 
     def backward(self, dq, dk, q, k, positions, dq_out=None, dk_out=None, need_weights: bool = True,
@@ -190,26 +203,28 @@ class AxialRotary:
         """Gradients by name: dq, dk, dwq, dwk (the weights', None without
         weights).  dq, dk: of the forward's outputs; q, k: the forward's inputs
         (read where there is a weight); dq_out, dk_out: as in the forward."""
-        M = int(dq.shape[0])
-        _rows(positions, (M, self.n_axes), torch.int32, "positions")
-        new = lambda t, o: torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) if o is None else o
-        dq_out, dk_out = new(dq, dq_out), new(dk, dk_out)
-        gdt = torch.float32 if grad_f32 else torch.bfloat16
-        vec = lambda w, t: torch.empty((self.D,), dtype=gdt, device=dq.device) if w is not None and need_weights and t.shape[1] else None
-        dwq, dwk = vec(self.q_weight, dq), vec(self.k_weight, dk)
-        xs = []
-        for t, g, w, what in ((q, dq, self.q_weight, "q"), (k, dk, self.k_weight, "k")):
-            if w is None:
-                xs += [None, 0]
-            else:
-                _shape(t, g.shape, what)
-                xs += [t, _head_ld(t, None, self.D, what)]
-        ws = None
+        if stream is not None:
+            with _on(stream):
+                return self.backward(dq, dk, q, k, positions, dq_out, dk_out, need_weights, grad_f32)
+        M = dq.shape[0]
+        _rows(positions, (M, self.n_axes), _I32, "positions")
+        if dq_out is None:
+            dq_out = dq.new_empty(dq.shape)
+        if dk_out is None:
+            dk_out = dk.new_empty(dk.shape)
+        qw, kw = self.q_weight, self.k_weight
+        gdt = _F32 if grad_f32 else _BF16
+        dwq = dq.new_empty((self.D,), dtype=gdt) if qw is not None and need_weights and dq.shape[1] else None
+        dwk = dk.new_empty((self.D,), dtype=gdt) if kw is not None and need_weights and dk.shape[1] else None
+        q, ldq = (None, 0) if qw is None else (q, _heads(q, M, dq.shape[1], self.D, "q"))
+        k, ldk = (None, 0) if kw is None else (k, _heads(k, M, dk.shape[1], self.D, "k"))
+        ws, size = None, 0
         if dwq is not None or dwk is not None:
-            ws = torch.empty((ops.fourtune_rope_workspace_bytes(self.table, M),), dtype=torch.uint8, device=dq.device)
-        ops.fourtune_rope_bwd(self.table, M, positions, self.eps, self._side(dq, dq_out, self.q_weight, "dq"),
-                              self._side(dk, dk_out, self.k_weight, "dk"), *xs, dwq, dwk,
-                              ops.FT_F32 if grad_f32 else ops.FT_BF16, ws, 0 if ws is None else ws.numel(), stream)
+            size = ops.fourtune_rope_workspace_bytes(self.table, M)
+            ws = dq.new_empty((size,), dtype=_U8)
+        ops.fourtune_rope_bwd(self.table, M, positions, self.eps, self._side(dq, dq_out, M, qw, "dq"),
+                              self._side(dk, dk_out, M, kw, "dk"), q, ldq, k, ldk, dwq, dwk,
+                              ops.FT_F32 if grad_f32 else ops.FT_BF16, ws, size)
         return dict(dq=dq_out, dk=dk_out, dwq=dwq, dwk=dwk)
 
 
@@ -227,36 +242,48 @@ class DocAttention:
         self.scale = self.D ** -0.5 if scale is None else float(scale)
 
     def desc(self, q, k, v, o, docs=None, prefix=None) -> ops.FtAttn:
-        M, Hq, Hkv = int(q.shape[0]), int(q.shape[1]), int(k.shape[1])
-        if k.shape[0] != M or v.shape[0] != M:
-            raise ValueError("q, k and v must have the same rows")
+        M, Hq = q.shape[:2]
+        Hkv, D = k.shape[1], self.D
         n_doc = _offsets(docs, "docs")
         if self.mask == ops.FT_MASK_PREFIX:
-            _rows(prefix, (n_doc,), torch.int32, "prefix")
             if prefix is None:
                 raise ValueError("the prefix mask needs the prefixes")
-        return ops.FtAttn(M, Hq, Hkv, self.D, self.mask, self.scale, self.softcap, n_doc, ops._ptr(docs),
-                          ops._ptr(prefix) if self.mask == ops.FT_MASK_PREFIX else None,
-                          _head_ld(q, Hq, self.D, "q"), _head_ld(k, Hkv, self.D, "k"),
-                          _head_ld(v, Hkv, self.D, "v"), _head_ld(o, Hq, self.D, "o"))
+            _rows(prefix, (n_doc,), _I32, "prefix")
+        else:
+            prefix = None
+        p = ops._ptr
+        return ops.FtAttn(M, Hq, Hkv, D, self.mask, self.scale, self.softcap, n_doc, p(docs), p(prefix),
+                          _heads(q, M, Hq, D, "q"), _heads(k, M, Hkv, D, "k"), _heads(v, M, Hkv, D, "v"),
+                          _heads(o, M, Hq, D, "o"))
 
     def forward(self, q, k, v, docs=None, prefix=None, need_lse: bool = True, stream=None):
         """(o [M, Hq, D], lse fp32 [Hq, M])"""
-        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device) if need_lse else None
-        ops.fourtune_attn_fwd(self.desc(q, k, v, o, docs, prefix), q, k, v, o, lse, stream)
+        if stream is not None:
+            with _on(stream):
+                return self.forward(q, k, v, docs, prefix, need_lse)
+        o = q.new_empty(q.shape)
+        lse = q.new_empty((q.shape[1], q.shape[0]), dtype=_F32) if need_lse else None
+        ops.fourtune_attn_fwd(self.desc(q, k, v, o, docs, prefix), q, k, v, o, lse)
         return o, lse
 
     def backward(self, do, q, k, v, o, lse, docs=None, prefix=None, dq=None, dk=None, dv=None, stream=None):
         """(dq, dk, dv), new tensors unless given (parts of one tensor, say)."""
-        new = lambda t, g: torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) if g is None else g
-        dq, dk, dv = new(q, dq), new(k, dk), new(v, dv)
+        if stream is not None:
+            with _on(stream):
+                return self.backward(do, q, k, v, o, lse, docs, prefix, dq, dk, dv)
+        if dq is None:
+            dq = q.new_empty(q.shape)
+        if dk is None:
+            dk = k.new_empty(k.shape)
+        if dv is None:
+            dv = v.new_empty(v.shape)
         d = self.desc(q, k, v, o, docs, prefix)
-        _rows(lse, (q.shape[1], q.shape[0]), torch.float32, "lse")
-        ws = torch.empty((ops.fourtune_attn_workspace_bytes(d),), dtype=torch.uint8, device=q.device)
-        ld = lambda t, h, what: _head_ld(t, h, self.D, what)
-        ops.fourtune_attn_bwd(d, do, ld(do, d.Hq, "do"), q, k, v, o, lse, dq, ld(dq, d.Hq, "dq"), dk,
-                              ld(dk, d.Hkv, "dk"), dv, ld(dv, d.Hkv, "dv"), ws, ws.numel(), stream)
+        M, Hq, Hkv, D = d.M, d.Hq, d.Hkv, d.D
+        _rows(lse, (Hq, M), _F32, "lse")
+        size = ops.fourtune_attn_workspace_bytes(d)
+        ws = q.new_empty((size,), dtype=_U8)
+        ops.fourtune_attn_bwd(d, do, _heads(do, M, Hq, D, "do"), q, k, v, o, lse, dq, _heads(dq, M, Hq, D, "dq"),
+                              dk, _heads(dk, M, Hkv, D, "dk"), dv, _heads(dv, M, Hkv, D, "dv"), ws, size)
         return dq, dk, dv
 
 
@@ -280,9 +307,10 @@ class AdamW:
             for t, what in ((p, "a parameter"), (g, "a gradient")) + (((w, "a master"),) if w is not None else ()):
                 if not t.is_contiguous() or t.numel() != p.numel() or t.device != params[0].device:
                     raise ValueError(f"{what} must be contiguous, of its parameter's size and on one device")
-            _is(w, torch.float32, "a master")
-            if p.dtype != params[0].dtype or g.dtype != grads[0].dtype:
-                raise TypeError("the parameters must be of one type, and so the gradients")
+            if w is not None and w.dtype is not _F32:
+                raise TypeError(f"a master must be {_F32}, not {w.dtype}")
+            if p.dtype != params[0].dtype or g.dtype != grads[0].dtype or p.dtype not in _DTYPES or g.dtype not in _DTYPES:
+                raise TypeError("the parameters must be of one type, bfloat16 or float32, and so the gradients")
         self.params, self.grads, self.masters = params, grads, masters
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.seed, self.steps = int(seed), 0
@@ -292,8 +320,8 @@ class AdamW:
                                           for p, g, w in zip(params, grads, masters)])
         size, total = ops.fourtune_adamw_plan_bytes(table, n)
         host = torch.empty((max(size, 1),), dtype=torch.uint8)
-        self.desc = ops.fourtune_adamw_plan(table, n, _dtype(params[0], "a parameter"), _dtype(grads[0], "a gradient"),
-                                            _STATES[state], host, host.numel())
+        self.desc = ops.fourtune_adamw_plan(table, n, _DTYPES[params[0].dtype], _DTYPES[grads[0].dtype], _STATES[state],
+                                            host, host.numel())
         self.table = host.to(dev)
         q8 = state == "q8"
         kinds = dict(m=(total, torch.uint8 if q8 else torch.float32), v=(total, torch.uint8 if q8 else torch.float32))
@@ -310,7 +338,8 @@ class AdamW:
     def step(self, grad_scale=None, stream=None):
         """One step; grad_scale: an fp32 device scalar that multiplies every
         gradient (a clipping factor), or None."""
-        _is(grad_scale, torch.float32, "grad_scale")
+        if grad_scale is not None and (grad_scale.dtype is not _F32 or grad_scale.numel() != 1):
+            raise TypeError("grad_scale must be one float32 value")
         self.steps += 1
         ops.fourtune_adamw_step(self.desc, self.steps, self.lr, *self.betas, self.eps, self.weight_decay, self.seed,
                                 grad_scale, stream)

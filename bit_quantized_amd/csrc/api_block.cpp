@@ -68,10 +68,10 @@ ft_status rope_table(const ft_rope* rp) {
     if (rp->axis[j] < 0 || rp->axis[j] >= rp->n_axes) return FT_EINVAL;
   return FT_OK;
 }
-ft_status rope_side(const ft_rope* rp, const ft_rope_side* s) {
+ft_status rope_side(const ft_rope* rp, const ft_rope_side* s, int64_t M) {
   if (!s) return FT_EINVAL;
   if (s->heads < 0 || s->heads > 65536) return FT_ESHAPE;
-  if (s->heads == 0) return FT_OK;
+  if (s->heads == 0 || M == 0) return FT_OK;
   if (!s->in || !s->out) return FT_EINVAL;
   const int64_t n = static_cast<int64_t>(s->heads) * rp->D;
   if (ft_status e = check_ld(s->ld_in, n); e != FT_OK) return e;
@@ -83,9 +83,9 @@ ft_status rope_check(const ft_rope* rp, int64_t M, const int32_t* pos, float eps
                      const ft_rope_side* q, const ft_rope_side* k) {
   if (ft_status e = rope_table(rp); e != FT_OK) return e;
   if (M < 0 || M > kMaxDim) return FT_ESHAPE;
-  if (!pos || !(eps >= 0.0f) || !std::isfinite(eps)) return FT_EINVAL;
-  if (ft_status e = rope_side(rp, q); e != FT_OK) return e;
-  if (ft_status e = rope_side(rp, k); e != FT_OK) return e;
+  if ((M > 0 && !pos) || !(eps >= 0.0f) || !std::isfinite(eps)) return FT_EINVAL;
+  if (ft_status e = rope_side(rp, q, M); e != FT_OK) return e;
+  if (ft_status e = rope_side(rp, k, M); e != FT_OK) return e;
   return aligned4(pos) ? FT_OK : FT_EALIGN;
 }
 ft::RopeArgs rope_args(const ft_rope* rp, int64_t M, const int32_t* pos, float eps,
@@ -171,10 +171,10 @@ extern "C" {
 ft_status fourtune_norm_fwd(const ft_norm* d, const void* x, const uint16_t* y, void* r,
                             uint16_t* h, float* stats, void* stream) {
   if (ft_status e = norm_shape(d); e != FT_OK) return e;
+  if (d->M == 0) return FT_OK;             // (tensors without elements may be null)
   if (!x || (y && !r) || (!y && !r && !h)) return FT_EINVAL;
   if (ft_status e = norm_factors(d, h != nullptr, y != nullptr); e != FT_OK) return e;
   if (bad16({x, y, r, h, stats})) return FT_EALIGN;
-  if (d->M == 0) return FT_OK;
   if (ft_status e = device_check(); e != FT_OK) return e;
   ft::NormArgs a = norm_args(d, h != nullptr, y != nullptr);
   a.x = x; a.y = y; a.r = r; a.h = h; a.stats = stats;
@@ -193,13 +193,15 @@ ft_status fourtune_norm_bwd(const ft_norm* d, const uint16_t* dh, const void* dr
                             void* dweight, void* dpost_weight, ft_dtype grad_dtype,
                             void* workspace, size_t ws_bytes, void* stream) {
   if (ft_status e = norm_shape(d); e != FT_OK) return e;
-  if (!dx || (!dh && !dr) || (!dh && !y)) return FT_EINVAL;
-  if (y && !dy) return FT_EINVAL;
-  if (dh && !r) return FT_EINVAL;
-  if (ft_status e = norm_factors(d, dh != nullptr, y != nullptr); e != FT_OK) return e;
-  if ((dh || (y && d->post_norm != FT_NORM_NONE)) && !stats) return FT_EINVAL;
-  if ((dscale || dshift || dweight) && !dh) return FT_EINVAL;
-  if ((dgate || dpost_weight) && !y) return FT_EINVAL;
+  if (d->M > 0) {                          // (tensors without elements may be null)
+    if (!dx || (!dh && !dr) || (!dh && !y)) return FT_EINVAL;
+    if (y && !dy) return FT_EINVAL;
+    if (dh && !r) return FT_EINVAL;
+    if (ft_status e = norm_factors(d, dh != nullptr, y != nullptr); e != FT_OK) return e;
+    if ((dh || (y && d->post_norm != FT_NORM_NONE)) && !stats) return FT_EINVAL;
+    if ((dscale || dshift || dweight) && !dh) return FT_EINVAL;
+    if ((dgate || dpost_weight) && !y) return FT_EINVAL;
+  }
   if (!is_dtype(grad_dtype)) return FT_EINVAL;
   if (bad16({dh, dr, r, y, stats, dx, dy, dscale, dshift, dgate, dweight, dpost_weight, workspace}))
     return FT_EALIGN;
@@ -286,8 +288,9 @@ ft_status fourtune_rope_bwd(const ft_rope* rp, int64_t M, const int32_t* positio
     const bool norm = s[i]->heads > 0 && s[i]->weight;
     if (dws[i] && !norm) return FT_EINVAL;
     if (!norm) continue;
-    if (!xs[i]) return FT_EINVAL;
-    if (ft_status e = check_ld(lds[i], static_cast<int64_t>(s[i]->heads) * rp->D); e != FT_OK) return e;
+    if (M > 0 && !xs[i]) return FT_EINVAL;
+    if (M > 0)
+      if (ft_status e = check_ld(lds[i], static_cast<int64_t>(s[i]->heads) * rp->D); e != FT_OK) return e;
     a.side[i].x = xs[i]; a.side[i].ld_x = lds[i]; a.side[i].dweight = dws[i];
   }
   if (bad16({q_x, k_x, dq_weight, dk_weight, workspace})) return FT_EALIGN;
@@ -307,9 +310,9 @@ ft_status fourtune_rope_bwd(const ft_rope* rp, int64_t M, const int32_t* positio
 ft_status fourtune_attn_fwd(const ft_attn* d, const uint16_t* q, const uint16_t* k,
                             const uint16_t* v, uint16_t* o, float* lse, void* stream) {
   if (ft_status e = attn_check(d); e != FT_OK) return e;
+  if (d->M == 0) return FT_OK;
   if (!q || !k || !v || !o) return FT_EINVAL;
   if (bad16({q, k, v, o, lse})) return FT_EALIGN;
-  if (d->M == 0) return FT_OK;
   if (ft_status e = device_check(); e != FT_OK) return e;
   ft::AttnArgs a = attn_args(d, q, k, v);
   a.o = o; a.lse = lse;
@@ -330,6 +333,7 @@ ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do
                             uint16_t* dk, int64_t ld_dk, uint16_t* dv, int64_t ld_dv,
                             void* workspace, size_t ws_bytes, void* stream) {
   if (ft_status e = attn_check(d); e != FT_OK) return e;
+  if (d->M == 0) return FT_OK;
   if (!d_o || !q || !k || !v || !o || !lse || !dq || !dk || !dv) return FT_EINVAL;
   const int64_t nq = static_cast<int64_t>(d->Hq) * d->D, nk = static_cast<int64_t>(d->Hkv) * d->D;
   if (ft_status e = attn_ld(ld_do, nq); e != FT_OK) return e;
@@ -339,7 +343,6 @@ ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do
   if (bad16({d_o, q, k, v, o, lse, dq, dk, dv, workspace})) return FT_EALIGN;
   if (ws_bytes < fourtune_attn_workspace_bytes(d)) return FT_EWORKSPACE;
   if (!workspace) return FT_EINVAL;
-  if (d->M == 0) return FT_OK;
   if (ft_status e = device_check(); e != FT_OK) return e;
   ft::AttnArgs a = attn_args(d, q, k, v);
   a.o_in = o; a.lse = const_cast<float*>(lse);
@@ -371,11 +374,16 @@ ft_status fourtune_adamw_plan(const ft_adamw_tensor* tensors, int32_t n_tensors,
   AdamwSizes s;
   if (!adamw_sizes(tensors, n_tensors, &s)) return FT_ESHAPE;
   if (table_bytes < s.bytes(n_tensors)) return FT_EWORKSPACE;
-  const bool master = tensors[0].master != nullptr;
-  if (master && param_dtype != FT_BF16) return FT_EINVAL;
+  int32_t masters = 0, live = 0;           // (a tensor without elements may have null pointers)
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    if (tensors[i].n == 0) continue;
+    ++live;
+    masters += tensors[i].master != nullptr;
+  }
+  const bool master = masters > 0;
+  if (master && (masters != live || param_dtype != FT_BF16)) return FT_EINVAL;
   for (int32_t i = 0; i < n_tensors; ++i) {
     const ft_adamw_tensor& t = tensors[i];
-    if ((t.master != nullptr) != master) return FT_EINVAL;
     if (t.n > 0 && (!t.p || !t.g)) return FT_EINVAL;
     if (bad16({t.p, t.g, t.master})) return FT_EALIGN;
   }

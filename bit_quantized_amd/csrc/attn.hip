@@ -10,8 +10,8 @@
 // exchange per tile and its statistics are one value per lane; and the
 // accumulator's rows are, in order, the reduction slots of O^T = V^T P^T, if
 // V's columns are read with the same order of rows.  So P never leaves its
-// registers.  P is rounded to bf16 for that product (relative 2^-9, as the
-// output is); scores, statistics and the output accumulate in fp32.
+// registers.  P is rounded to bf16 for that product (at most 2^-8
+// of it, as the output is); scores, statistics and the output accumulate in fp32.
 #include "attn_dev.hpp"
 
 namespace ft {

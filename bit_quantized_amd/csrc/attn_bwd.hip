@@ -14,7 +14,7 @@
 // no traffic of partial dQ.  As in the forward each wave owns 32 rows, the
 // scores are computed with the owned rows as columns, so that a lane's
 // accumulator is the operand of the product that follows, and P and dS are
-// rounded to bf16 there (relative 2^-9).
+// rounded to bf16 there (at most 2^-8 of each).
 #include "attn_dev.hpp"
 
 namespace ft {

@@ -27,8 +27,11 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// sin and cos of position p times the frequency hi + lo (turns).
+// sin and cos of position p times the frequency hi + lo (turns).  No
+// contraction: r - rint(r) taken as one fused operation on p * hi would hold
+// the rounding error e of r already.
 __device__ __forceinline__ void turn(float p, float hi, float lo, float& s, float& c) {
+#pragma clang fp contract(off)
   const float r = p * hi;
   const float e = __builtin_fmaf(p, hi, -r);
   const float f = (r - __builtin_rintf(r)) + __builtin_fmaf(p, lo, e);

@@ -6,4 +6,4 @@ include/fourtune.h).  `bit_quantized_amd.ops` is the thin ctypes binding;
 package does not load the library; the first call through `ops` does, and
 fails loudly if it is not built.
 """
-__all__ = ["ops", "synth", "layer", "block"]
+__all__ = ["ops", "synth", "layer", "block", "dit"]

@@ -3,12 +3,18 @@
 //   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
 //   p = decay p - rate m / (sqrt(v) lift + eps)
 //
-// Memory bound: 22 to 28 bytes an element with 32-bit states, 8 to 10 with
-// 8-bit ones.  A workgroup takes 2048 elements of one tensor, found through
+// Memory bound: 22 to 28 bytes an element with 32-bit states, 10 to 14 with
+// 8-bit ones (whose codes and random bits cost about as long in the vector
+// units as their bytes take to move).  A workgroup takes 2048 elements of one tensor, found through
 // a table of chunks made once for the set of tensors, so that the grid is
 // full however the elements are spread over tensors; a thread takes eight
 // consecutive elements (16-byte accesses), and 16 threads the 128 elements
 // of a block of 8-bit states, whose new scale is a maximum over 16 lanes.
+//
+// Measured: 36 M elements in 320 tensors with 32-bit states, masters and
+// bf16 parameters 189 us (5.4 TB/s; a large copy reaches 5.1); 101 M with
+// 8-bit states, no masters 192 us (5.3 TB/s; 257 us before the codes went
+// through fp32's denormals and the root through its short form).
 //
 // The 8-bit states are the exact same function of the inputs on every
 // machine that rounds fp32 operations correctly, so no operation on their
@@ -29,25 +35,42 @@ constexpr float kMostV = 31.0f * 16384.0f;    // 4 exponent bits
 constexpr float kTiny = 1e-35f;               // a block below this is zero
 
 // What a code (sign taken off) stands for, in units of the smallest code.
-// As an fp32 bit pattern the code's exponent and fraction are in place at
-// bit 19; 2^(126 - ...) is added to the exponent field, and the lowest
-// exponent has no leading one.
-__device__ __forceinline__ float code_value(uint32_t c) {
-  const uint32_t e = c >> 4;
-  const float f = __uint_as_float((c << 19) + (130u << 23));    // (1 + f/16) 2^(e + 3)
-  return e ? f : static_cast<float>(c);
+// An fp32 number with the code at bit 19 has the code's exponent, fraction
+// and, as a denormal, its missing leading one, 2^-130 as large.
+__device__ __forceinline__ float code_value(uint32_t at19) {
+  return __builtin_ldexpf(__uint_as_float(at19), 130);
 }
-// y >= 0 in those units to a code: `bits` (19) are added below the last
-// kept bit, then the rest is cut.  Below 16 (no leading one) y + 16 has its
-// last bit where the codes of [16, 32) have theirs.
-__device__ __forceinline__ uint32_t code_of(float y, uint32_t bits, uint32_t top) {
-  const bool low = y < 16.0f;
-  const float z = low ? y + 16.0f : y;
-  // (16 + f) 2^(e - 1) has the exponent field 131 + (e - 1): the field minus
-  // 130 is the code's exponent, one less where 16 was added
-  const uint32_t u = (__float_as_uint(z) + bits) >> 19;
-  const uint32_t c = u - (130u << 4) - (low ? 16u : 0u);
-  return c < top ? c : top;
+// y >= 0 in those units to a code: 2^-130 y has the code at bit 19 (with the
+// rounding of fp32's denormals where the code has no leading one); `bits`
+// (19) are added below and the rest is cut.
+//
+// Where value and bits meet a code exactly (once in 2^19), fp32's rounding
+// of the value has already taken the choice from the sum, and either code
+// is right.  It is taken as the plain form of perf/operators.py takes it on
+// this card, whose fp64 powers 2^-4, 2^-9, 2^-12 and 2^-14 (kTieDown) come
+// out a unit low and so leave the lower code: the states of the two are then
+// the same bits, step after step, and can be compared as such.
+constexpr uint32_t kTieDown = 1u << 5 | 1u << 10 | 1u << 13 | 1u << 15;    // at the codes' exponents, one more
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t bits) {
+  const uint32_t at = __float_as_uint(__builtin_ldexpf(y, -130));
+  return (at + bits + __builtin_amdgcn_sbfe(kTieDown, at >> 23, 1)) >> 19;
+}
+// The correctly rounded root of 2^-90 <= v < 2^126: s = v / sqrt(v) by the
+// hardware's estimate and one of Newton's steps from the exact residual
+// (Markstein's method; all mantissas of both parities were compared with
+// 64-bit roots).  A third of the instructions of the general root.
+__device__ __forceinline__ float root_of(float v) {
+  const float y = __builtin_amdgcn_rsqf(v);
+  const float s = v * y;
+  return __builtin_fmaf(__builtin_fmaf(-s, s, v), 0.5f * y, s);
+}
+// Maximum of each aligned group of 16 lanes, in every lane of it.
+__device__ __forceinline__ uint32_t lanes16_max(uint32_t x) {
+  const auto with = [](uint32_t y, float z) { return max(y, __float_as_uint(z)); };
+  x = with(x, dpp<0xB1>(__uint_as_float(x)));
+  x = with(x, dpp<0x4E>(__uint_as_float(x)));
+  x = with(x, dpp<0x141>(__uint_as_float(x)));
+  return with(x, dpp<0x140>(__uint_as_float(x)));
 }
 __device__ __forceinline__ uint32_t mix(uint32_t i, uint32_t key) {
   uint32_t h = i * 0x9E3779B1u + key;
@@ -93,18 +116,27 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
     }
   }
   if constexpr (Q8) {
-    const u32x2 mc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.m) + at);
-    const u32x2 vc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.v) + at);
+    u32x2 mc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.m) + at);
+    u32x2 vc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.v) + at);
+    if (left < 8) {                               // zeros past the tensor
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int64_t n = left - 4 * w;
+        const uint32_t keep = n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
+        mc[w] &= keep;
+        vc[w] &= keep;
+      }
+    }
     const float ms = a.m_scale[at >> 7] * (1.0f / kMostM);
     const float vs = a.v_scale[at >> 7] * (1.0f / kMostV);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t cm = (mc[e >> 2] >> (8 * (e & 3))) & 0xFFu;
       const uint32_t cv = (vc[e >> 2] >> (8 * (e & 3))) & 0xFFu;
-      const float mv = code_value(cm & 127u) * ms;
-      const float rv = code_value(cv) * vs;
-      m[e] = e < left ? (cm & 128u ? -mv : mv) : 0.0f;
-      v[e] = e < left ? rv * rv : 0.0f;
+      const uint32_t at19 = (cm << 24 & 0x80000000u) | (cm << 19 & 0x03F80000u);    // with the sign
+      const float rv = code_value(cv << 19) * vs;
+      m[e] = code_value(at19) * ms;
+      v[e] = rv * rv;
     }
   } else {
     // (the arena runs on to a multiple of 128 past the tensor)
@@ -117,14 +149,37 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
       v[e] = vr.get(e);
     }
   }
-  float root[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float gg = g[e] * gs;
     m[e] = m[e] * a.b1 + gg * a.b1c;
     v[e] = v[e] * a.b2 + (gg * gg) * a.b2c;
-    root[e] = Q8 ? __builtin_sqrtf(v[e]) : __builtin_amdgcn_sqrtf(v[e]);
-    p[e] = p[e] * a.decay - (m[e] * __builtin_amdgcn_rcpf(root[e] * a.lift + a.eps)) * a.rate;
+  }
+  float root[8];
+  if constexpr (Q8) {
+    uint32_t least = ~0u, most = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      least = min(least, __float_as_uint(v[e]));
+      most = max(most, __float_as_uint(v[e]));
+    }
+    if (least >= (127u - 90u) << 23 && most < (127u + 126u) << 23) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) root[e] = root_of(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) root[e] = __builtin_sqrtf(v[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) root[e] = __builtin_amdgcn_sqrtf(v[e]);
+  }
+  // (the parameter is no state that decides later roundings: a unit of fp32
+  // in the quotient is far below the step's own)
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float by = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(root[e], a.lift, a.eps));
+    p[e] = __builtin_fmaf(-by, a.rate, p[e] * a.decay);
   }
   uint32_t rnd[8];
   if constexpr (Q8 || P == 1) {
@@ -132,23 +187,26 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
     for (int e = 0; e < 8; ++e) rnd[e] = mix(static_cast<uint32_t>(at) + e, a.key);
   }
   if constexpr (Q8) {
-    float mm = 0.0f, vm = 0.0f;
+    // (maxima of bit patterns: a NaN is above all, and stays as its block's
+    // scale, so that no gradient's NaN is lost in the codes)
+    uint32_t mb = 0, vb = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      mm = fmaxf(mm, __builtin_fabsf(m[e]));
-      vm = fmaxf(vm, root[e]);
+      mb = max(mb, __float_as_uint(__builtin_fabsf(m[e])));
+      vb = max(vb, __float_as_uint(__builtin_fabsf(root[e])));
     }
-    mm = lanes_max<16>(mm);
-    vm = lanes_max<16>(vm);
+    const float mm = __uint_as_float(lanes16_max(mb));
+    const float vm = __uint_as_float(lanes16_max(vb));
     const float mu = mm > kTiny ? (1.0f / mm) * kMostM : 0.0f;
     const float vu = vm > kTiny ? (1.0f / vm) * kMostV : 0.0f;
     u32x2 mc = {0, 0}, vc = {0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      uint32_t cm = code_of(__builtin_fabsf(m[e]) * mu, rnd[e] >> 13, 127u);
-      cm |= m[e] < 0.0f ? 128u : 0u;
-      uint32_t cv = code_of(root[e] * vu, (rnd[e] * 0x9E3779B1u) >> 13, 255u);
-      cv = cv == 0u && root[e] > 0.0f ? 1u : cv;
+      uint32_t cm = min(code_of(__builtin_fabsf(m[e]) * mu, rnd[e] >> 13), 127u);
+      cm |= __float_as_uint(m[e]) >> 24 & 128u;
+      // a root above zero keeps a code above zero
+      const uint32_t cv = min(max(code_of(root[e] * vu, (rnd[e] * 0x9E3779B1u) >> 13),
+                                  min(__float_as_uint(root[e]), 1u)), 255u);
       mc[e >> 2] |= cm << (8 * (e & 3));
       vc[e >> 2] |= cv << (8 * (e & 3));
     }

@@ -28,17 +28,6 @@ __device__ __forceinline__ float lanes_sum(float x) {
   if constexpr (N >= 64) x += __shfl_xor(x, 32);
   return x;
 }
-template <int N>
-__device__ __forceinline__ float lanes_max(float x) {
-  if constexpr (N >= 2) x = fmaxf(x, dpp<0xB1>(x));
-  if constexpr (N >= 4) x = fmaxf(x, dpp<0x4E>(x));
-  if constexpr (N >= 8) x = fmaxf(x, dpp<0x141>(x));
-  if constexpr (N >= 16) x = fmaxf(x, dpp<0x140>(x));
-  if constexpr (N >= 32) x = fmaxf(x, __shfl_xor(x, 16));
-  if constexpr (N >= 64) x = fmaxf(x, __shfl_xor(x, 32));
-  return x;
-}
-
 // Eight values as they lie in memory: bf16 (F32 = 0) or fp32 (1).
 template <int F32>
 struct Raw8;

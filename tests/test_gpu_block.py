@@ -533,6 +533,22 @@ def test_adamw_8bit_states(param):
         assert new["m_scale"][(512 + 128) // 128] == 0 and np.all(new["v"][640:768] == 0)
 
 
+def test_adamw_8bit_states_at_the_ends_of_the_range():
+    """Roots far below and above common ones, and a NaN or Inf among a block's gradients, which stays to be seen."""
+    sizes = [1e-17, 1e-15, 1e-13, 1.0, 1e18, 1e19]                          # their squares: 1e-34 to 1e38
+    g = torch.tensor(sizes, dtype=F32, device=DEV).repeat_interleave(128)
+    g = torch.cat([g, torch.ones(256, dtype=F32, device=DEV)])
+    g[6 * 128 + 5], g[7 * 128 + 6] = float("nan"), float("inf")
+    opt = block.AdamW([torch.zeros_like(g)], [g], lr=1e-3, betas=(0.0, 0.0), eps=1e-30, weight_decay=0.0, state="q8", seed=5)
+    opt.step()
+    m, r = f64(opt.arena["m_scale"]), f64(opt.arena["v_scale"])
+    want = f64(g)[:768:128]
+    assert np.all(np.abs(m[:6] - want) <= 2.0 ** -23 * want)
+    assert np.all(np.abs(r[:6] - want) <= 2.0 ** -23 * want)               # g g and its root, half a unit each
+    assert np.all(opt.arena["v"].cpu().numpy()[:768] >= 254)               # the largest, or one below at a tie
+    assert np.isnan(m[6]) and np.isnan(r[6]) and np.isinf(m[7]) and np.isinf(r[7])
+
+
 def test_adamw_random_rounding_keeps_small_steps():
     """A bf16 parameter without a master moves by a step far below its spacing, on average over elements
     and steps; the mean's deviation is that of independent roundings."""

@@ -4,7 +4,7 @@
 //
 // A workgroup of four or eight waves (wide_tiles()) takes 128 or 256 queries
 // of one document and head, a wave 32 of them; key and value tiles of 64 rows
-// go through LDS, the next tile's loads in flight while one is worked on.  The products run as
+// go through LDS, loaded one or two tiles ahead.  The products run as
 // 32x32x16 bf16 matrix instructions on the transposed problem: S^T = K Q^T
 // leaves a query's scores in two lanes (32 apart), so the softmax needs one
 // exchange per tile and its statistics are one value per lane; and the
@@ -12,6 +12,17 @@
 // V's columns are read with the same order of rows.  So P never leaves its
 // registers.  P is rounded to bf16 for that product (at most 2^-8
 // of it, as the output is); scores, statistics and the output accumulate in fp32.
+//
+// A tile costs a wave about as long in the vector units (exponentials, sums,
+// maxima: 750 cycles) as in the matrix unit (1024), and both are there for
+// all waves of a SIMD at once.  Four waves that run freely overlap them by
+// chance: 53% of the cycles have a matrix product at work (24 heads of 128,
+// 4608 keys).  With eight waves, the two of a SIMD take turns: a barrier
+// splits a tile's time in half, in which four waves have their products and
+// four their softmax, and the products' LDS reads are ordered to run eight
+// products ahead: 64%, and 15% fewer cycles.  The clock pays most of that
+// back (2.2 -> 2.0 GHz: the card is at its power), so the time falls by 6%:
+// 268 -> 252 us, 1.04 PFLOP/s; a large bf16 matrix product runs at 1.57.
 #include "attn_dev.hpp"
 
 namespace ft {
@@ -24,13 +35,15 @@ constexpr int BN = 64;
 
 // NW waves of 32 queries each.
 template <int D, bool CAP, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
+__global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
   constexpr int KS = D / 16, DB = D / 32, BM = 32 * NW;
   constexpr int TB = BN * D * 2;         // bytes of a tile
   // (two objects: with one, the compiler waits for all loads in flight before
   // the transposing reads)
-  __shared__ __attribute__((aligned(16))) uint8_t klds[2 * TB];
-  __shared__ __attribute__((aligned(16))) uint8_t vlds[2 * TB];
+  constexpr bool TURNS = NW == 8;        // half of the waves in turn with the others
+  constexpr int NB = TURNS ? 3 : 2;
+  __shared__ __attribute__((aligned(16))) uint8_t klds[NB * TB];
+  __shared__ __attribute__((aligned(16))) uint8_t vlds[NB * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
@@ -56,14 +69,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint3
   const int nt = (seen + BN - 1) / BN;
   const uint16_t* kp = a.k + static_cast<int64_t>(dt.lo) * a.ld_k + kvh * D;
   const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
-  const uint32_t lane0 = stage_lane<D>(lane);
-  auto fetch = [&](int t) {
-    const int buf = (t & 1) * TB;
-    stage<D, BN, NW>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, klds + buf, wave, lane, lane0);
-    stage<D, BN, NW>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, vlds + buf, wave, lane,
-                    lane0);
-  };
-  fetch(0);
+  const Stager<D, BN, NW> ks(a.ld_k, wave, lane), vs(a.ld_v, wave, lane);
+  auto fetch_k = [&](int t, int buf) { ks(kp, t, len, klds + buf * TB); };
+  auto fetch_v = [&](int t, int buf) { vs(vp, t, len, vlds + buf * TB); };
+  fetch_k(0, 0);
+  fetch_v(0, 0);
+  if constexpr (TURNS) fetch_k(1, 1);
   u32x4 q[KS];
   {
     const uint16_t* qrow = a.q + static_cast<int64_t>(qi) * a.ld_q + head * D;
@@ -74,7 +85,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint3
     }
   }
   const uint32_t kbase = row_base<D>(l32, half), vbase = col_base<D>(lane);
-  f32x16 o[DB];
+  f32x16 o[DB], s[2];
+  u32x4 p[4];
 #pragma unroll
   for (int db = 0; db < DB; ++db) o[db] = zero16();
   float m = kNegInf, l = 0.0f;
@@ -82,12 +94,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint3
   const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
   const float c2 = a.softcap * kLog2e;
   const int wq0 = q0 + wave * 32;                        // the wave's first query
-  staged_barrier();
-  for (int t = 0; t < nt; ++t) {
-    if (t + 1 < nt) fetch(t + 1);
-    const uint8_t* kt = klds + (t & 1) * TB;
-    const uint8_t* vt = vlds + (t & 1) * TB;
-    f32x16 s[2];
+  auto scores = [&](int buf) {
+    const uint8_t* kt = klds + buf * TB;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       s[kb] = zero16();
@@ -95,6 +103,34 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint3
       for (int ks = 0; ks < KS; ++ks)
         s[kb] = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + (kbase ^ row_step(ks))), q[ks], s[kb]);
     }
+  };
+  auto outputs = [&](int buf) {
+    const uint8_t* vt = vlds + buf * TB;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* vk = vt + (kb * 32 + h * 16) * 2 * D;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+          o[db] = mfma_bf16_32x32x16(col_read(vk, vbase ^ col_step<D>(db, 0), vbase ^ col_step<D>(db, 1)), p[2 * kb + h], o[db]);
+      }
+  };
+  // In the turns' products the reads run AHEAD products before their use.
+  auto order = [] {
+    constexpr int PV = 4 * DB, QK = 2 * KS, AHEAD = 8;   // two reads a product, one read
+#define FT_ORDER(what, n) __builtin_amdgcn_sched_group_barrier(what, n, 0)
+    constexpr int PRODUCT = 0x8, READ = 0x100;
+    FT_ORDER(READ, 2 * AHEAD);
+#pragma unroll
+    for (int j = 0; j < PV + QK; ++j) {
+      FT_ORDER(PRODUCT, 1);
+      if (j + AHEAD < PV) FT_ORDER(READ, 2);
+      else if (j + AHEAD < PV + QK) FT_ORDER(READ, 1);
+    }
+#undef FT_ORDER
+  };
+  auto softmax = [&](int t) {
     if constexpr (CAP) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
@@ -143,15 +179,79 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(const AttnArgs a, uint3
       }
       l += sum;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 p = pack8(s[kb], 8 * h);
-        const uint8_t* vk = vt + (kb * 32 + h * 16) * 2 * D;
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-          o[db] = mfma_bf16_32x32x16(col_read(vk, vbase ^ col_step<D>(db, 0), vbase ^ col_step<D>(db, 1)), p, o[db]);
-      }
+      for (int h = 0; h < 2; ++h) p[2 * kb + h] = pack8(s[kb], 8 * h);
     }
+  };
+  if constexpr (!TURNS) {
     staged_barrier();
+    for (int t = 0; t < nt; ++t) {
+      if (t + 1 < nt) {
+        fetch_k(t + 1, (t + 1) & 1);
+        fetch_v(t + 1, (t + 1) & 1);
+      }
+      scores(t & 1);
+      softmax(t);
+      outputs(t & 1);
+      staged_barrier();
+    }
+  } else {
+    // Step t of the first half of the waves: products (outputs of tile t - 1,
+    // scores of tile t), barrier, softmax of t, barrier; of the second half:
+    // softmax of t - 1, barrier, products, barrier.  So K of t and V of t - 1
+    // are read during step t; K of t + 2 and V of t + 1 are loaded in it,
+    // into the third buffers, and waited for at the end of step t + 1.
+    constexpr int IN = 2 * Stager<D, BN, NW>::N;          // loads of a wave in a step
+    int b0 = 2, b1 = 0, b2 = 1;                           // the buffers of tiles t - 1, t and t + 1
+    auto turn = [&] {
+      const int b = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = b;
+    };
+    staged_barrier<IN / 2>();                             // (all but the last loads: K of tile 1)
+    if (wave < NW / 2) {
+      scores(0);
+      staged_barrier<63>();
+      fetch_k(2, b0);
+      fetch_v(1, b2);
+      softmax(0);
+      staged_barrier<IN>();
+      turn();
+      for (int t = 1; t < nt; ++t) {
+        outputs(b0);
+        scores(b1);
+        order();
+        staged_barrier<63>();
+        fetch_k(t + 2, b0);
+        fetch_v(t + 1, b2);
+        softmax(t);
+        staged_barrier<IN>();
+        turn();
+      }
+      outputs(b0);
+    } else {
+      fetch_k(2, b0);
+      fetch_v(1, b2);
+      staged_barrier<63>();
+      scores(0);
+      staged_barrier<IN>();
+      turn();
+      for (int t = 1; t < nt; ++t) {
+        fetch_k(t + 2, b0);
+        fetch_v(t + 1, b2);
+        softmax(t - 1);
+        staged_barrier<63>();
+        outputs(b0);
+        scores(b1);
+        order();
+        staged_barrier<IN>();
+        turn();
+      }
+      softmax(nt - 1);
+      outputs(b0);
+    }
+    // no load may land in LDS after the workgroup has left it
+    __builtin_amdgcn_s_waitcnt(0x0F70);
   }
   l = halves_sum(l);
   const float inv = 1.0f / l;

@@ -15,6 +15,13 @@
 // scores are computed with the owned rows as columns, so that a lane's
 // accumulator is the operand of the product that follows, and P and dS are
 // rounded to bf16 there (at most 2^-8 of each).
+//
+// Bound by the matrix units and the power they draw: 62% (dQ) and 53% (dK,
+// dV) of the cycles have a product at work, at 1.8 to 2.0 GHz.  LDS reads are
+// issued two to four products ahead of their use (dK, dV 1037 -> 977 us, dQ
+// 713 -> 706 us at two documents of 4608 tokens, 24 heads of 128: 1.07 and
+// 1.11 PFLOP/s; a large bf16 product runs at 1.57).  Workgroups of eight waves
+// that share their key tiles gained dQ 2% at some sizes and lost 6% at others.
 #include "attn_dev.hpp"
 
 namespace ft {
@@ -135,11 +142,30 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       f32x16 s = zero16(), dp = zero16();
+      constexpr int A1 = 4, A2 = 4;                      // products (pairs of them) that reads are ahead
+      u32x4 rk[A1], rv[A1], rc[A2];
+      auto rows = [&](int ks) {
+        rk[ks % A1] = lds_read_b128(kt + kb * 32 * 2 * D + (rbase ^ row_step(ks)));
+        rv[ks % A1] = lds_read_b128(vt + kb * 32 * 2 * D + (rbase ^ row_step(ks)));
+      };
+      auto columns = [&](int i) {
+        const uint8_t* kk = kt + (kb * 32 + i / DB * 16) * 2 * D;
+        rc[i % A2] = col_read(kk, cbase ^ col_step<D>(i % DB, 0), cbase ^ col_step<D>(i % DB, 1));
+      };
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int ks = 0; ks < A1; ++ks) rows(ks);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        s = mfma_bf16_32x32x16(lds_read_b128(kt + kb * 32 * 2 * D + (rbase ^ row_step(ks))), q[ks], s);
-        dp = mfma_bf16_32x32x16(lds_read_b128(vt + kb * 32 * 2 * D + (rbase ^ row_step(ks))), g[ks], dp);
+        __builtin_amdgcn_sched_barrier(0);
+        s = mfma_bf16_32x32x16(rk[ks % A1], q[ks], s);
+        dp = mfma_bf16_32x32x16(rv[ks % A1], g[ks], dp);
+        if (ks + A1 < KS) rows(ks + A1);
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < A2; ++i) columns(i);
+      __builtin_amdgcn_sched_barrier(0);
       if constexpr (CAP) tanh16(s, c1);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -158,10 +184,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4 d = pack8(s, 8 * h);
-        const uint8_t* kk = kt + (kb * 32 + h * 16) * 2 * D;
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
-          acc[db] = mfma_bf16_32x32x16(col_read(kk, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1)), d, acc[db]);
+        for (int db = 0; db < DB; ++db) {
+          const int i = h * DB + db;
+          __builtin_amdgcn_sched_barrier(0);
+          acc[db] = mfma_bf16_32x32x16(rc[i % A2], d, acc[db]);
+          if (i + A2 < 2 * DB) columns(i + A2);
+        }
       }
     }
     staged_barrier();
@@ -291,11 +320,27 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
     for (int qb = 0; qb < BQ / 32; ++qb) {
       __builtin_amdgcn_sched_barrier(0);
       f32x16 s = zero16(), dp = zero16();
+      constexpr int A1 = 2, A2 = CAP && D == 128 ? 2 : 4;                      // products (pairs of them) that reads are ahead
+      u32x4 rq[A1], rg[A1], rv[A1], rc[A2];
+      auto rows = [&](int ks) {
+        rq[ks % A1] = lds_read_b128(qt + qb * 32 * 2 * D + (rbase ^ row_step(ks)));
+        rg[ks % A1] = lds_read_b128(gt + qb * 32 * 2 * D + (rbase ^ row_step(ks)));
+        rv[ks % A1] = lds_read_b128(vl + (rbase ^ row_step(ks)));
+      };
+      // operand i of the second products: rows h = i / (2 DB), columns db; dO, then Q
+      auto columns = [&](int i) {
+        const uint8_t* at = (i & 1 ? qt : gt) + (qb * 32 + i / (2 * DB) * 16) * 2 * D;
+        const int db = (i >> 1) % DB;
+        rc[i % A2] = col_read(at, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1));
+      };
+#pragma unroll
+      for (int ks = 0; ks < A1; ++ks) rows(ks);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        s = mfma_bf16_32x32x16(lds_read_b128(qt + qb * 32 * 2 * D + (rbase ^ row_step(ks))), k[ks], s);
-        dp = mfma_bf16_32x32x16(lds_read_b128(gt + qb * 32 * 2 * D + (rbase ^ row_step(ks))),
-                                lds_read_b128(vl + (rbase ^ row_step(ks))), dp);
+        __builtin_amdgcn_sched_barrier(0);
+        s = mfma_bf16_32x32x16(rq[ks % A1], k[ks], s);
+        dp = mfma_bf16_32x32x16(rg[ks % A1], rv[ks % A1], dp);
+        if (ks + A1 < KS) rows(ks + A1);
       }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (CAP) tanh16(s, c1);
@@ -311,6 +356,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
           s[4 * j + e] = __builtin_fmaf(x, c2, -lse2[e]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < A2; ++i) columns(i);
+      __builtin_amdgcn_sched_barrier(0);
       if (edge) {
         // key > query: hidden, unless in the prefix
         const int e = first_seen - t * BQ - qb * 32 - 4 * half;
@@ -329,11 +378,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4 pp = pack8(s, 8 * h), dd = pack8(dp, 8 * h);
-        const uint32_t at = (qb * 32 + h * 16) * 2 * D;
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
-          dv[db] = mfma_bf16_32x32x16(col_read(gt + at, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1)), pp, dv[db]);
-          dk[db] = mfma_bf16_32x32x16(col_read(qt + at, cbase ^ col_step<D>(db, 0), cbase ^ col_step<D>(db, 1)), dd, dk[db]);
+          const int i = (h * DB + db) * 2;
+          __builtin_amdgcn_sched_barrier(0);
+          dv[db] = mfma_bf16_32x32x16(rc[i % A2], pp, dv[db]);
+          if (i + A2 < 4 * DB) columns(i + A2);
+          __builtin_amdgcn_sched_barrier(0);
+          dk[db] = mfma_bf16_32x32x16(rc[(i + 1) % A2], dd, dk[db]);
+          if (i + 1 + A2 < 4 * DB) columns(i + 1 + A2);
         }
       }
     }
@@ -381,18 +434,13 @@ __global__ __launch_bounds__(256) void k_attn_dkv_sum(const AttnArgs a) {
   *reinterpret_cast<u32x2*>(out) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
 }
 
-template <int D, bool CAP, int NW>
-hipError_t dq_go(const AttnArgs& a, hipStream_t st) {
+template <int D, bool CAP>
+hipError_t go(const AttnArgs& a, hipStream_t st) {
+  constexpr int NW = 4, BQ = 32;
   const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
   hipLaunchKernelGGL((k_attn_dq<D, CAP, NW>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0, st, a,
                      tiles);
-  return hipGetLastError();
-}
-template <int D, bool CAP>
-hipError_t go(const AttnArgs& a, hipStream_t st) {
-  if (hipError_t e = wide_tiles(a) ? dq_go<D, CAP, 8>(a, st) : dq_go<D, CAP, 4>(a, st); e != hipSuccess) return e;
-  constexpr int NW = 4, BQ = 32;
-  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (attn_split_heads(a.M, a.Hq, a.Hkv)) {
     hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ, true>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW),
                        0, st, a, tiles);

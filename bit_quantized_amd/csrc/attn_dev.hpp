@@ -99,15 +99,17 @@ inline int64_t tiles_of(const AttnArgs& a) {
   return a.doc ? a.M / BM + a.n_doc + 2 : (a.M + BM - 1) / BM;
 }
 
-// Workgroups of eight waves (256 rows) or of four (128): the registers allow
-// eight waves on a CU either way.  Eight that share the tiles they walk are
-// faster while a CU has all eight (7%: half the loads and barriers), but a
-// last round that would fill at most half of the CUs goes faster as twice
-// as many workgroups of four, and so do problems of less than one round.
+// Whether the forward's workgroups have eight waves (256 queries) that take
+// turns, or four (128) that do not.  Eight are faster while most CUs have
+// them (24 heads of 128, full mask: 73 -> 61 us at 2048 queries, 0.75 rounds
+// of the 256 CUs; 287 -> 252 at 4608, 1.7 rounds; 1581 -> 1539 at 11469, 4.2),
+// but a last round of few lets the others idle for longer than fours would
+// (141 -> 149 at 2730, 1.03 rounds; 216 -> 221 at 4096, 1.5).  Under a causal
+// or prefix mask the lengths differ and the rounds blur (166 -> 162 at 4096).
 inline bool wide_tiles(const AttnArgs& a) {
-  const int64_t rounds256 = a.M * a.Hq;                  // times 256 rows, 256 CUs
-  const int64_t part = rounds256 % (256 * 256);
-  return rounds256 >= 256 * 256 && (part == 0 || part > 128 * 256);
+  const int64_t n = a.M * a.Hq, round = 256 * 256;      // rows, rows of one round
+  const int64_t rounds = (n + round - 1) / round;
+  return 2 * n > round && (a.mask != 0 || rounds == 1 || 4 * n > 3 * rounds * round);
 }
 
 // A tile of rows in LDS: 2 D bytes a row, its 16-byte chunks permuted by
@@ -161,6 +163,29 @@ __device__ __forceinline__ void stage(const uint16_t* p, int64_t ld, int have, u
     dma16(r, tile + first * (2 * D), at + static_cast<uint32_t>(first) * row_bytes + (lane0 ^ flip));
   }
 }
+// The same for tile after tile of one matrix, with the lanes' offsets kept.
+template <int D, int ROWS, int NW>
+struct Stager {
+  static constexpr int CH = D / 8, RI = 64 / CH, N = ROWS / RI / NW;
+  static_assert(N * RI * NW == ROWS, "the waves share the tile evenly");
+  uint32_t off[N], row_bytes, dest;
+  __device__ __forceinline__ Stager(int64_t ld, int wave, int lane)
+      : row_bytes(uniform(static_cast<uint32_t>(ld) * 2u)), dest(wave * N * RI * 2 * D) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t first = (wave * N + i) * RI;
+      off[i] = (first + lane / CH) * row_bytes + (stage_lane<D>(lane) ^ (swz<D>(first) << 4));
+    }
+  }
+  // tile t of the matrix of `rows` rows at p
+  __device__ __forceinline__ void operator()(const uint16_t* p, int t, int rows, uint8_t* tile) const {
+    const int have = max(0, min(rows - t * ROWS, ROWS));
+    const uint8_t* at = reinterpret_cast<const uint8_t*>(p) + static_cast<int64_t>(t) * (ROWS * row_bytes);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(uniform(at), uniform(static_cast<uint32_t>(have) * row_bytes));
+#pragma unroll
+    for (int i = 0; i < N; ++i) dma16(r, tile + dest + i * RI * 2 * D, off[i]);
+  }
+};
 // Wait until at most VM of this wave's loads are in flight (and none of its
 // LDS accesses), then for the workgroup.  (Builtins: the compiler counts the
 // waits, too, and adds none of its own for the loads that are done.)

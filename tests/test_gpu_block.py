@@ -381,6 +381,24 @@ def test_attention_wide_workgroups(D):
                     [0] * 4, "causal", 0.0)
 
 
+@pytest.mark.parametrize("D,mask,cap", [(64, "full", 0.0), (64, "prefix", 20.0), (128, "full", 20.0), (128, "prefix", 0.0)])
+def test_attention_wide_workgroups_masks(D, mask, cap):
+    """The same with other masks and a cap; documents of one tile and of several, none longer than the last tile."""
+    M, H = 600, 96
+    rng = np.random.default_rng(D + len(mask))
+    q, k, v, do = (draw(rng, M, H, D) for _ in range(4))
+    starts, prefix = [0, 1, 65, 257, 257, 600], [1, 64, 70, 0, 150]
+    off = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    pre = torch.tensor(prefix, dtype=torch.int32, device=DEV) if mask == "prefix" else None
+    op = block.DocAttention(D, mask=mask, softcap=cap)
+    o, lse = op.forward(q, k, v, docs=off, prefix=pre)
+    dq, dk, dv = op.backward(do, q, k, v, o, lse, docs=off, prefix=pre)
+    for h in (0, 50, 95):
+        s = slice(h, h + 1)
+        _attn_check(q[:, s], k[:, s], v[:, s], do[:, s], o[:, s], lse[s], dq[:, s], dk[:, s], dv[:, s], starts,
+                    prefix if pre is not None else [0] * 5, mask, cap)
+
+
 def test_attention_documents_do_not_touch():
     """NaN and Inf in one document leave the others' bits as they are."""
     M, H, D = 400, 2, 64

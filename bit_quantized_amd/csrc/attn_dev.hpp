@@ -99,8 +99,12 @@ inline int64_t tiles_of(const AttnArgs& a) {
   return a.doc ? a.M / BM + a.n_doc + 2 : (a.M + BM - 1) / BM;
 }
 
-// Whether the forward's workgroups have eight waves (256 queries) that take
-// turns, or four (128) that do not.  Eight are faster while most CUs have
+// Whether the workgroups' lengths differ: under a causal or prefix mask, and
+// among the documents of a packed batch.
+inline bool uneven(const AttnArgs& a) { return a.mask != 0 || a.n_doc > 2; }
+
+// Whether the forward's workgroups of heads of 128 have eight waves (256
+// queries) that take turns, or four (128) that do not.  Eight are faster while most CUs have
 // them (24 heads of 128, full mask: 73 -> 61 us at 2048 queries, 0.75 rounds
 // of the 256 CUs; 287 -> 252 at 4608, 1.7 rounds; 1581 -> 1539 at 11469, 4.2),
 // but a last round of few lets the others idle for longer than fours would

@@ -451,12 +451,11 @@ def test_attention_offsets_past_32_bits():
     op = block.DocAttention(D)
     o, lse = op.forward(q, k, v, docs=off)
     sq, sk, sv = (tail[:, i * D:(i + 1) * D].unflatten(1, (1, D)) for i in range(3))
-    so, slse = op.forward(sq, sk, sv)
-    assert torch.equal(o[M - 150:], so) and torch.equal(lse[:, M - 150:], slse)
     assert float(o[:M - 150].float().abs().max()) == 0
     grads = op.backward(o, q, k, v, o, lse, docs=off)
-    small = op.backward(so, sq, sk, sv, so, slse)
-    assert all(torch.equal(a[M - 150:], b) for a, b in zip(grads, small))
+    assert all(float(t[:M - 150].float().abs().max()) == 0 for t in grads)
+    to = o[M - 150:]
+    _attn_check(sq, sk, sv, to, to, lse[:, M - 150:], *(t[M - 150:] for t in grads), [0, 150], [0], "full", 0.0)
     # the rotation and the norm on the same rows
     rot = block.AxialRotary(D, [D])
     pos = torch.arange(M, dtype=torch.int32, device=DEV)[:, None].contiguous()

@@ -2,9 +2,9 @@
 //   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i . k_j (capped by a tanh)
 // in one pass over the keys with the running maximum and sum of each query.
 //
-// A workgroup takes 64, 128 or 256 queries of one document and head, a wave 32
-// of them; where there are few workgroups, two groups of waves take the same
-// queries and every other key tile each, and are joined at the end (their
+// A workgroup takes 32 to 256 queries of one document and head, a wave 32
+// of them; where there are few workgroups, groups of waves take the same
+// queries and divide the key tiles, and are joined at the end (their
 // maxima, sums and outputs through LDS).  Key and value tiles of 64 rows
 // go through LDS, loaded one or two tiles ahead.  The products run as
 // 32x32x16 bf16 matrix instructions on the transposed problem: S^T = K Q^T
@@ -33,13 +33,15 @@ using namespace attn_dev;
 
 namespace {
 
-constexpr int BN = 64;
+// Registers for two waves a SIMD, also where LDS leaves one: more than 256
+// would be of two kinds, with moves between them (5 to 20% slower).
+#pragma clang diagnostic ignored "-Wpass-failed"
 
-// NW waves of 32 queries each, in G groups that divide the key tiles.
-template <int D, bool CAP, int NW, int G>
-__global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
+// NW waves of 32 queries each, in G groups that divide the tiles of BN keys.
+template <int D, bool CAP, int NW, int G, int BN>
+__global__ __launch_bounds__(64 * NW, D == 64 && NW == 8 ? 4 : 2) void k_attn_fwd(const AttnArgs a, uint32_t tiles) {
   constexpr int W = NW / G;              // waves of a group
-  constexpr int KS = D / 16, DB = D / 32, BM = 32 * W;
+  constexpr int KS = D / 16, DB = D / 32, KB = BN / 32, BM = 32 * W;
   constexpr int TB = BN * D * 2;         // bytes of a tile
   // (two objects: with one, the compiler waits for all loads in flight before
   // the transposing reads)
@@ -89,8 +91,8 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
     }
   }
   const uint32_t kbase = row_base<D>(l32, half), vbase = col_base<D>(lane);
-  f32x16 o[DB], s[2];
-  u32x4 p[4];
+  f32x16 o[DB], s[KB];
+  u32x4 p[2 * KB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) o[db] = zero16();
   float m = -3e38f, l = 0.0f;           // (finite: a group may see only hidden keys of a query)
@@ -101,7 +103,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
   auto scores = [&](int buf) {
     const uint8_t* kt = klds + (buf * G + group) * TB;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < KB; ++kb) {
       s[kb] = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
   auto outputs = [&](int buf) {
     const uint8_t* vt = vlds + (buf * G + group) * TB;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint8_t* vk = vt + (kb * 32 + h * 16) * 2 * D;
@@ -122,7 +124,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
   };
   // In the turns' products the reads run AHEAD products before their use.
   auto order = [] {
-    constexpr int PV = 4 * DB, QK = 2 * KS, AHEAD = 8;   // two reads a product, one read
+    constexpr int PV = 2 * KB * DB, QK = KB * KS, AHEAD = 8;   // two reads a product, one read
 #define FT_ORDER(what, n) __builtin_amdgcn_sched_group_barrier(what, n, 0)
     constexpr int PRODUCT = 0x8, READ = 0x100;
     FT_ORDER(READ, 2 * AHEAD);
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
   auto softmax = [&](int t) {
     if constexpr (CAP) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         tanh16(s[kb], c1);
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[kb][r] *= c2;
@@ -148,14 +150,14 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
       // the tile's keys from `end` on are hidden from this lane's query
       const int end = (a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix))) - t * BN - 4 * half;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (kb * 32 + acc_row(r) >= end) s[kb][r] = kNegInf;
     }
     float mt = s[0][0];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[kb][r]);
     mt = halves_max(mt);
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
         for (int r = 0; r < 16; ++r) o[db][r] *= f;
     }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < KB; ++kb) {
       float sum = 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -309,30 +311,40 @@ __global__ __launch_bounds__(64 * NW, D == 64 && NW >= 8 ? 4 : 2) void k_attn_fw
   }
 }
 
-template <int D, int NW, int G>
+template <int D, int NW, int G, int BN = 64>
 hipError_t go(const AttnArgs& a, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW / G>(a));
   const dim3 grid(tiles * static_cast<uint32_t>(a.Hq));
-  if (a.softcap > 0) hipLaunchKernelGGL((k_attn_fwd<D, true, NW, G>), grid, dim3(64 * NW), 0, st, a, tiles);
-  else hipLaunchKernelGGL((k_attn_fwd<D, false, NW, G>), grid, dim3(64 * NW), 0, st, a, tiles);
+  if (a.softcap > 0) hipLaunchKernelGGL((k_attn_fwd<D, true, NW, G, BN>), grid, dim3(64 * NW), 0, st, a, tiles);
+  else hipLaunchKernelGGL((k_attn_fwd<D, false, NW, G, BN>), grid, dim3(64 * NW), 0, st, a, tiles);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // Workgroups of W waves by G groups.  What counts is how many of the 256 CUs
-// have work and how evenly: small problems take 64 queries and share the keys
-// between two groups (12 heads of 64, 1024 keys: 17.4 us with 128 queries and
-// one group, 14.3 with two, 12.2 with 64 queries; 24 heads of 128, 512 keys:
-// 15.2, 14.8, 13.5), up to one workgroup a CU, or where documents and masks
+// have work, and how long a workgroup's walk over the keys is.
+// Up to one workgroup a CU, a single wave owns 32 queries and four groups
+// share the keys (64 queries by two groups / 32 by four: 2 heads of 64, 4096
+// keys 31.9 / 25.2 us, 8 heads, 1024 keys 11.6 / 10.5, 256 keys 5.9 / 6.2;
+// heads of 128, whose tiles for four groups are 32 keys: 8 heads, 1024 keys
+// 18.6 / 16.2, 512 keys 12.1 / 11.3, and by two groups of one wave 11.0).
+// Then 64 queries by two groups (12 heads of 64, 1024 keys: 128 queries 17.4
+// us, by two groups 14.3, 64 by two 12.2; 24 heads of 128, 512 keys: 15.2,
+// 14.8, 13.5), up to one workgroup a CU, or where documents and masks
 // make their lengths differ up to two (of heads of 64; 2711 tokens in eight
 // documents, 12 heads: 37, 32, 22 us).  Heads of 64 take two groups
 // always (24 heads, 4608 keys: 176 -> 170 us; causal 115 -> 102), heads of 128
 // up to one workgroup a CU (1024 keys: 26.9 -> 24.3 us; 1365 keys, more than
 // one: 48 -> 56).
 hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st) {
-  const int64_t n64 = (a.M + 63) / 64 * a.Hq, n128 = (a.M + 127) / 128 * a.Hq;
-  if (D == 64) return n64 <= 256 || (uneven(a) && a.M * a.Hq <= 512 * 64) ? go<64, 4, 2>(a, st) : go<64, 8, 2>(a, st);
+  const int64_t n32 = (a.M + 31) / 32 * a.Hq, n64 = (a.M + 63) / 64 * a.Hq, n128 = (a.M + 127) / 128 * a.Hq;
+  const int64_t each = a.M / a.n_doc;
+  if (D == 64) {
+    if (n32 <= 256 && each > 256) return go<64, 4, 4>(a, st);
+    return n64 <= 256 || (uneven(a) && a.M * a.Hq <= 512 * 64) ? go<64, 4, 2>(a, st) : go<64, 8, 2>(a, st);
+  }
+  if (n32 <= 256) return each > 640 ? go<128, 4, 4, 32>(a, st) : go<128, 2, 2>(a, st);
   if (n64 <= 256) return go<128, 4, 2>(a, st);
   if (n128 <= 256) return go<128, 8, 2>(a, st);
   return wide_tiles(a) ? go<128, 8, 1>(a, st) : go<128, 4, 1>(a, st);

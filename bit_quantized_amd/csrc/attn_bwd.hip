@@ -8,10 +8,10 @@
 // as the values); there (up to 1024 keys) the sum over the keys is taken.
 //
 // Two kernels, so that every sum has one owner and a fixed order (no
-// atomics): k_attn_dq walks the keys of 64 or 128 queries and also leaves
-// delta; k_attn_dkv walks the queries of 64 or 128 keys, over all query heads
-// of the key head.  Where there are few workgroups, two groups of waves walk
-// every other tile each and are joined at the end.
+// atomics): k_attn_dq walks the keys of 32 to 128 queries and also leaves
+// delta; k_attn_dkv walks the queries of 32 to 128 keys, over all query heads
+// of the key head.  Where there are few workgroups, groups of waves divide the
+// tiles and are joined at the end.
 // S and dP are formed in both: 7 products of M^2 D instead of 5, for
 // no traffic of partial dQ.  As in the forward each wave owns 32 rows, the
 // scores are computed with the owned rows as columns, so that a lane's
@@ -31,37 +31,46 @@ using namespace attn_dev;
 
 namespace {
 
-constexpr int kFewTiles = 16;            // of 64 keys
+// Registers for two waves a SIMD, also where LDS leaves one: more than 256
+// would be of two kinds, with moves between them (5 to 20% slower).
+#pragma clang diagnostic ignored "-Wpass-failed"
 
-// The sums of two groups of W waves, in the first: the second's through LDS,
-// 4 W DB KiB of it, which nobody reads any more.
-template <int DB, int W>
+constexpr int kFewKeys = 1024;
+
+// The sums of G groups of W waves, in the first: half of the groups to the
+// other half at a time, through LDS (G / 2 W DB times 4 KiB that nobody reads
+// any more).
+template <int DB, int W, int G>
 __device__ __forceinline__ void join_groups(f32x16 (&acc)[DB], uint8_t* lds, int group, int w, int lane) {
-  f32x4* const part = reinterpret_cast<f32x4*>(lds) + w * (DB * 4 * 64) + lane;
-  if (group == 1) {
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+  for (int h = G / 2; h >= 1; h /= 2) {
+    f32x4* const part = reinterpret_cast<f32x4*>(lds) + (group % h * W + w) * (DB * 4 * 64) + lane;
+    if (group >= h && group < 2 * h) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        part[(db * 4 + i) * 64] = f32x4{acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]};
-  }
-  __syncthreads();
-  if (group == 0) {
+      for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+        for (int i = 0; i < 4; ++i)
+          part[(db * 4 + i) * 64] = f32x4{acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]};
+    }
+    __syncthreads();
+    if (group < h) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 v = part[(db * 4 + i) * 64];
+      for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[db][4 * i + e] += v[e];
-      }
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 v = part[(db * 4 + i) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[db][4 * i + e] += v[e];
+        }
+    }
+    if (h > 1) __syncthreads();
   }
 }
 
-// NW waves of 32 queries each, in G groups that divide the key tiles.
-template <int D, bool CAP, int NW, int G>
+// NW waves of 32 queries each, in G groups that divide the tiles of BN keys.
+template <int D, bool CAP, int NW, int G, int BN>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32_t tiles) {
-  constexpr int KS = D / 16, DB = D / 32, BN = 64, W = NW / G, BM = 32 * W;
+  constexpr int KS = D / 16, DB = D / 32, KB = BN / 32, W = NW / G, BM = 32 * W;
   constexpr int TB = BN * D * 2;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * G * TB];   // [buffer][K, V][group]
   __shared__ float sums[2][NW][32];
@@ -130,14 +139,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
   const int wq0 = q0 + w0;
   int end = a.mask == 0 ? len : min(len, max(wq0 + l32 + 1, dt.prefix));
   staged_barrier();
-  if (nt <= kFewTiles) {
+  if (nt * BN <= kFewKeys) {
     // delta = sum p dP / sum p, by a pass over the keys of its own
     float psum = 0.0f, pdp = 0.0f;
     for (int i = 0; i < steps; ++i) {
       if (i + 1 < steps) fetch(i + 1);
       const int t = i * G + group;
       const uint8_t* kt = lds + ((i & 1) * 2 * G + group) * TB;
-      for (int kb = 0; kb < 2 && t < nt; ++kb) {
+      for (int kb = 0; kb < KB && t < nt; ++kb) {
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -187,7 +196,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
     const int last = t * BN + BN - 1;
     const bool edge = last >= len || (a.mask != 0 && last > wq0 && last >= dt.prefix);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < KB; ++kb) {
       if (G > 1 && t >= nt) break;
       f32x16 s = zero16(), dp = zero16();
       constexpr int A1 = 4, A2 = 4;                      // products (pairs of them) that reads are ahead
@@ -243,7 +252,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
     }
     staged_barrier();
   }
-  if constexpr (G > 1) join_groups<DB, W>(acc, lds, group, wave % W, lane);
+  if constexpr (G > 1) join_groups<DB, W, G>(acc, lds, group, wave % W, lane);
   if (live && group == 0) {
 #pragma unroll
     for (int db = 0; db < DB; ++db)
@@ -458,9 +467,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
     staged_barrier();
   }
   if constexpr (G > 1) {
-    join_groups<DB, W>(dk, lds, part, w, lane);
+    join_groups<DB, W, G>(dk, lds, part, w, lane);
     __syncthreads();
-    join_groups<DB, W>(dv, lds, part, w, lane);
+    join_groups<DB, W, G>(dv, lds, part, w, lane);
   }
   if (live && part == 0) {
 #pragma unroll
@@ -502,10 +511,10 @@ __global__ __launch_bounds__(256) void k_attn_dkv_sum(const AttnArgs a) {
   *reinterpret_cast<u32x2*>(out) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
 }
 
-template <int D, bool CAP, int NW, int G>
+template <int D, bool CAP, int NW, int G, int BN = 64>
 hipError_t dq_go(const AttnArgs& a, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW / G>(a));
-  hipLaunchKernelGGL((k_attn_dq<D, CAP, NW, G>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0, st, a,
+  hipLaunchKernelGGL((k_attn_dq<D, CAP, NW, G, BN>), dim3(tiles * static_cast<uint32_t>(a.Hq)), dim3(64 * NW), 0, st, a,
                      tiles);
   return hipGetLastError();
 }
@@ -525,27 +534,45 @@ hipError_t dkv_go(const AttnArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 // Workgroups of W waves by G groups, by how many there are for 256 CUs, as in
-// the forward.  24 heads, full mask, 128 rows and one group / two groups / 64
-// rows and two groups, us:
-//   dQ     heads of 64:   512 keys 19.4 / 19.2 / 14.4, 2048 57 / 61 / 54, 4096 162 / 172 / 183
-//          heads of 128:  512 keys 29.5 / 28.8 / 23.3, 1024 54 / 50 / 74, 1365 62 / 73 / 87
-//   dK, dV heads of 64:   512 keys 18.3 / 15.1 / 12.0, 2048 81 / 88 / 80, 6144 604 / 637 / 609
-//          heads of 128:  512 keys 27.3 / 23.9 / 18.9, 1024 50 / 41 / 58, 1365 82 / 94 / 109
-//          (causal, 2048 keys 115 / 92 / 114)
-// and 2711 tokens in eight documents, 12 query and 4 key heads of 64: dQ 72 /
-// 44 / 40, dK, dV 55 / 41 / 34.
+// the forward.  Full mask, us:
+//   rows x groups          128x1  128x2  64x2   32x4
+//   dQ     2 heads of 64, 4096 keys                38.8   31.5
+//          24 heads of 64, 512  19.4   19.2  14.4
+//          the same, 2048       57     61    54
+//          the same, 4096       162    172   183
+//          8 heads of 128, 1024              35.4   28.3
+//          24 heads of 128, 512 29.5   28.8  23.3
+//          the same, 1024       54     50    74
+//          the same, 1365       62     73    87
+//   dK, dV 8 heads of 64, 2048               36.9   28.6
+//          16 heads of 64, 1536              37.4   38.5
+//          24 heads of 64, 512  18.3   15.1  12.0
+//          the same, 6144       604    637   609
+//          8 heads of 128, 1024              28.3   21.7
+//          24 heads of 128, 512 27.3   23.9  18.9
+//          the same, 1024       50     41    58
+//          the same, 1365       82     94    109
+//          causal, 2048         115    92    114
+// and short documents have no use for many groups (dK, dV of 32 keys, 2 heads
+// of 128: 9.8 us by four groups, 8.0 by two).
 template <int D, bool CAP>
 hipError_t go(const AttnArgs& a, hipStream_t st) {
   const int64_t heads = attn_split_heads(a.M, a.Hq, a.Hkv) ? a.Hq : a.Hkv;       // of dK and dV
-  const int64_t t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
+  const int64_t t32 = (a.M + 31) / 32, t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
+  const int64_t each = a.M / a.n_doc;
   if constexpr (D == 64) {
-    hipError_t e = a.M * a.Hq <= 768 * 64 ? dq_go<D, CAP, 4, 2>(a, st) : dq_go<D, CAP, 4, 1>(a, st);
-    return e != hipSuccess ? e : dkv_go<D, CAP, 4, 2>(a, st);
+    hipError_t e = t32 * a.Hq <= 256 && each > 128 ? dq_go<D, CAP, 4, 4>(a, st)
+                   : a.M * a.Hq <= 768 * 64        ? dq_go<D, CAP, 4, 2>(a, st)
+                                                   : dq_go<D, CAP, 4, 1>(a, st);
+    if (e != hipSuccess) return e;
+    return t32 * heads <= (a.mask != 0 && !a.doc ? 1024 : 512) && each > 64 ? dkv_go<D, CAP, 4, 4>(a, st) : dkv_go<D, CAP, 4, 2>(a, st);
   } else {
-    hipError_t e = t64 * a.Hq <= 256    ? dq_go<D, CAP, 4, 2>(a, st)
+    hipError_t e = t32 * a.Hq <= 256    ? dq_go<D, CAP, 4, 4, 32>(a, st)
+                   : t64 * a.Hq <= 256  ? dq_go<D, CAP, 4, 2>(a, st)
                    : t128 * a.Hq <= 256 ? dq_go<D, CAP, 8, 2>(a, st)
                                         : dq_go<D, CAP, 4, 1>(a, st);
     if (e != hipSuccess) return e;
+    if (t32 * heads <= 256) return each > 128 ? dkv_go<D, CAP, 4, 4>(a, st) : dkv_go<D, CAP, 2, 2>(a, st);
     if (t64 * heads <= 256) return dkv_go<D, CAP, 4, 2>(a, st);
     return t128 * heads <= (uneven(a) ? 512 : 256) ? dkv_go<D, CAP, 8, 2>(a, st) : dkv_go<D, CAP, 4, 1>(a, st);
   }

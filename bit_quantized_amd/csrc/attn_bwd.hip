@@ -37,6 +37,12 @@ namespace {
 
 constexpr int kFewKeys = 1024;
 
+// The workgroups of two waves, which take documents of a few tokens, take P
+// and dS as two bf16 each: few terms leave each rounding to be seen, and the
+// products cost nothing beside the latencies.
+template <int NW>
+constexpr bool fine = NW == 2;
+
 // The sums of G groups of W waves, in the first: half of the groups to the
 // other half at a time, through LDS (G / 2 W DB times 4 KiB that nobody reads
 // any more).
@@ -240,12 +246,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs a, uint32
       for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r]) * dp[r];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const u32x4 d = pack8(s, 8 * h);
+        const u32x4 d = pack8(s, 8 * h), rest = fine<NW> ? rest8(s, 8 * h, d) : u32x4{};
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
           const int i = h * DB + db;
           __builtin_amdgcn_sched_barrier(0);
           acc[db] = mfma_bf16_32x32x16(rc[i % A2], d, acc[db]);
+          if constexpr (fine<NW>) acc[db] = mfma_bf16_32x32x16(rc[i % A2], rest, acc[db]);
           if (i + A2 < 2 * DB) columns(i + A2);
         }
       }
@@ -450,14 +457,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dkv(const AttnArgs a, uint3
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4 pp = pack8(s, 8 * h), dd = pack8(dp, 8 * h);
+        const u32x4 pr = fine<NW> ? rest8(s, 8 * h, pp) : u32x4{}, dr = fine<NW> ? rest8(dp, 8 * h, dd) : u32x4{};
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
           const int i = (h * DB + db) * 2;
           __builtin_amdgcn_sched_barrier(0);
           dv[db] = mfma_bf16_32x32x16(rc[i % A2], pp, dv[db]);
+          if constexpr (fine<NW>) dv[db] = mfma_bf16_32x32x16(rc[i % A2], pr, dv[db]);
           if (i + A2 < 4 * DB) columns(i + A2);
           __builtin_amdgcn_sched_barrier(0);
           dk[db] = mfma_bf16_32x32x16(rc[(i + 1) % A2], dd, dk[db]);
+          if constexpr (fine<NW>) dk[db] = mfma_bf16_32x32x16(rc[(i + 1) % A2], dr, dk[db]);
           if (i + 1 + A2 < 4 * DB) columns(i + 1 + A2);
         }
       }
@@ -561,13 +571,16 @@ hipError_t go(const AttnArgs& a, hipStream_t st) {
   const int64_t t32 = (a.M + 31) / 32, t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
   const int64_t each = a.M / a.n_doc;
   if constexpr (D == 64) {
-    hipError_t e = t32 * a.Hq <= 256 && each > 128 ? dq_go<D, CAP, 4, 4>(a, st)
-                   : a.M * a.Hq <= 768 * 64        ? dq_go<D, CAP, 4, 2>(a, st)
-                                                   : dq_go<D, CAP, 4, 1>(a, st);
+    hipError_t e = t32 * a.Hq <= 256        ? each > 128 ? dq_go<D, CAP, 4, 4>(a, st) : dq_go<D, CAP, 2, 2>(a, st)
+                   : a.M * a.Hq <= 768 * 64 ? dq_go<D, CAP, 4, 2>(a, st)
+                                            : dq_go<D, CAP, 4, 1>(a, st);
     if (e != hipSuccess) return e;
-    return t32 * heads <= (a.mask != 0 && !a.doc ? 1024 : 512) && each > 64 ? dkv_go<D, CAP, 4, 4>(a, st) : dkv_go<D, CAP, 4, 2>(a, st);
+    if (t32 * heads <= 256 && each <= 128) return dkv_go<D, CAP, 2, 2>(a, st);
+    return t32 * heads <= (a.mask != 0 && !a.doc ? 1024 : 512) && each > 64 ? dkv_go<D, CAP, 4, 4>(a, st)
+                                                                            : dkv_go<D, CAP, 4, 2>(a, st);
   } else {
-    hipError_t e = t32 * a.Hq <= 256    ? dq_go<D, CAP, 4, 4, 32>(a, st)
+    hipError_t e = t32 * a.Hq <= 256 && each <= 64 ? dq_go<D, CAP, 2, 2>(a, st)
+                   : t32 * a.Hq <= 256  ? dq_go<D, CAP, 4, 4, 32>(a, st)
                    : t64 * a.Hq <= 256  ? dq_go<D, CAP, 4, 2>(a, st)
                    : t128 * a.Hq <= 256 ? dq_go<D, CAP, 8, 2>(a, st)
                                         : dq_go<D, CAP, 4, 1>(a, st);

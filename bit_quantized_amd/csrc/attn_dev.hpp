@@ -281,6 +281,15 @@ __device__ __forceinline__ u32x4 pack8(const f32x16& s, int first) {
   return w;
 }
 
+// What is left of those values beside the operand w: together 16 bits of them.
+__device__ __forceinline__ u32x4 rest8(const f32x16& s, int first, const u32x4& w) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = cvt_pk_bf16(s[first + 2 * i] - bf16lo_to_f32(w[i]), s[first + 2 * i + 1] - bf16hi_to_f32(w[i]));
+  return r;
+}
+
 // Where value r of a 32x32 accumulator lies: row acc_row(r) + 4 (lane / 32).
 constexpr int acc_row(int r) { return 8 * (r >> 2) + (r & 3); }
 

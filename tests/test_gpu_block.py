@@ -399,6 +399,30 @@ def test_attention_wide_workgroups_masks(D, mask, cap):
                     prefix if pre is not None else [0] * 5, mask, cap)
 
 
+@pytest.mark.parametrize("D,M,Hq,Hk,mask,cap", [
+    (64, 40, 4, 2, "causal", 0.0), (128, 100, 2, 1, "prefix", 0.0),            # two groups of one wave
+    (64, 700, 2, 1, "prefix", 20.0), (128, 700, 2, 2, "causal", 20.0),         # four groups of one wave
+    (64, 260, 20, 10, "full", 0.0), (128, 330, 32, 16, "prefix", 0.0),         # two groups of 64 rows
+    (64, 900, 24, 24, "full", 20.0), (128, 700, 20, 20, "causal", 0.0),        # two groups of 128 rows
+    (64, 1400, 36, 36, "causal", 0.0), (128, 900, 40, 20, "full", 0.0),        # 128 rows, one group or two
+])
+def test_attention_by_the_size_of_the_problem(D, M, Hq, Hk, mask, cap):
+    """The workgroups' shapes go by the rows times the heads; a document of them ends inside every kind of tile."""
+    rng = np.random.default_rng(M + Hq)
+    q, k, v, do = draw(rng, M, Hq, D), draw(rng, M, Hk, D), draw(rng, M, Hk, D), draw(rng, M, Hq, D)
+    prefix = torch.tensor([M // 3], dtype=torch.int32, device=DEV) if mask == "prefix" else None
+    op = block.DocAttention(D, mask=mask, softcap=cap)
+    o, lse = op.forward(q, k, v, prefix=prefix)
+    dq, dk, dv = op.backward(do, q, k, v, o, lse, prefix=prefix)
+    for g in {0, Hk - 1}:
+        r = Hq // Hk
+        hs, gs = slice(r * g, r * g + r), slice(g, g + 1)
+        _attn_check(q[:, hs], k[:, gs], v[:, gs], do[:, hs], o[:, hs], lse[hs], dq[:, hs], dk[:, gs], dv[:, gs], [0, M],
+                    [M // 3 if prefix is not None else 0], mask, cap)
+    o2, _ = op.forward(q, k, v, prefix=prefix, need_lse=False)
+    assert torch.equal(o, o2) and all(torch.equal(a, b) for a, b in zip((dq, dk, dv), op.backward(do, q, k, v, o, lse, prefix=prefix)))
+
+
 def test_attention_documents_do_not_touch():
     """NaN and Inf in one document leave the others' bits as they are."""
     M, H, D = 400, 2, 64

@@ -235,7 +235,9 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
   uint32_t lowp[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    if constexpr (P == 1) lowp[e] = (__float_as_uint(p[e]) + ((rnd[e] * 0x510E527Fu) >> 16)) >> 16;
+    // (a NaN keeps its upper half: bits added to it could carry out of it)
+    if constexpr (P == 1)
+      lowp[e] = (__float_as_uint(p[e]) + (p[e] == p[e] ? (rnd[e] * 0x510E527Fu) >> 16 : 0u)) >> 16;
     else lowp[e] = 0;
   }
   if (left >= 8) {

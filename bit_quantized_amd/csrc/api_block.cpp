@@ -111,8 +111,9 @@ ft_status attn_shape(const ft_attn* d) {
   if (d->D != 64 && d->D != 128) return FT_ESHAPE;
   if (d->Hq < 1 || d->Hkv < 1 || d->Hq > 1024 || d->Hq % d->Hkv != 0) return FT_ESHAPE;
   if (d->n_doc < 1 || d->n_doc > (1 << 20) || (!d->doc && d->n_doc != 1)) return FT_ESHAPE;
-  // tiles of at least 64 rows, times heads, are one grid
-  if ((d->M / 64 + d->n_doc + 2) * d->Hq > (int64_t(1) << 30)) return FT_ESHAPE;
+  // tiles of 64 rows, times heads, are one grid of workgroups of up to 512
+  // threads, which are counted in 32 bits (smaller tiles are for small problems)
+  if ((d->M / 64 + d->n_doc + 2) * d->Hq > (int64_t(1) << 22)) return FT_ESHAPE;
   return FT_OK;
 }
 // Rows reach at most 64 strides in 32-bit offsets.
@@ -159,7 +160,7 @@ bool adamw_sizes(const ft_adamw_tensor* t, int32_t n, AdamwSizes* s) {
     if (t[i].n < 0 || t[i].n > kArenaMax) return false;
     s->arena += up128(t[i].n);
     s->chunks += (t[i].n + ft::kAdamwChunk - 1) / ft::kAdamwChunk;
-    if (s->arena > kArenaMax) return false;
+    if (s->arena > kArenaMax || s->chunks > (int64_t(1) << 23)) return false;
   }
   return true;
 }

@@ -12,7 +12,7 @@
 // are as long as a row, are read once for all of them.
 //
 // Measured at 9216 rows of 3072 in bf16, gate and LayerNorm: 43.5 us, 5.2 TB/s
-// (a large copy reaches 5.06); with one row at a time 54 us, with four 48.
+// (a large copy reaches 5.06).
 // At 4608 rows without y 15.2 us (3.7 TB/s, the launch and one row's latency).
 #include <algorithm>
 
@@ -34,7 +34,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void k_norm_fwd(const NormArgs a) {
   const int waves = static_cast<int>(blockDim.x >> 6);
   const int nv = static_cast<int>(a.C >> 3);
   const float inv_c = 1.0f / static_cast<float>(a.C);
-  const int lo = static_cast<int>(blockIdx.x) * R;
+  const int lo = static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x) * R;
+  if (lo >= a.M) return;
   const int hi = min(lo + R, static_cast<int>(a.M));
   int at[NV];
   bool ok[NV];
@@ -186,7 +187,9 @@ __global__ __launch_bounds__(kMaxWaves * 64) void k_norm_fwd(const NormArgs a) {
 template <int NV, int R, int F32, int Y>
 hipError_t go(const NormArgs& a, hipStream_t st) {
   const int64_t per = 512 * NV;                        // channels of a wave
-  const dim3 grid(static_cast<uint32_t>((a.M + R - 1) / R));
+  // (a grid's x times its workgroup's has 32 bits)
+  const uint32_t wgs = static_cast<uint32_t>((a.M + R - 1) / R), wide = std::min(wgs, 1u << 20);
+  const dim3 grid(wide, (wgs + wide - 1) / wide);
   const dim3 block(static_cast<uint32_t>(64 * ((a.C + per - 1) / per)));
   hipLaunchKernelGGL((k_norm_fwd<NV, R, F32, Y>), grid, block, 0, st, a);
   return hipGetLastError();

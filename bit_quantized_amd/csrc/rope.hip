@@ -244,10 +244,12 @@ __global__ __launch_bounds__(kQuads* kWays) void k_rope_reduce(const RopeArgs a,
 }
 
 // With weight gradients a wave walks several rows, so that at most 1024
-// workgroups leave partial sums.
-constexpr int64_t kMaxPart = 1024;
+// workgroups leave partial sums; without, where a grid of one row a wave would
+// pass the 32 bits that its threads are counted in.
+constexpr int64_t kMaxPart = 1024, kMaxWgs = 1 << 22;
 int rows_per_wave(int64_t M, bool part) {
-  return part ? static_cast<int>((M + kMaxPart * kWaves - 1) / (kMaxPart * kWaves)) : 1;
+  const int64_t per = (part ? kMaxPart : kMaxWgs) * kWaves;
+  return static_cast<int>((M + per - 1) / per);
 }
 
 template <int LPH>

@@ -400,7 +400,7 @@ typedef enum { FT_NORM_NONE = 0, FT_NORM_RMS = 1, FT_NORM_LAYER = 2 } ft_norm_ki
  * device pointers.  Without y, the fields of r's formula are not read. */
 typedef struct {
   int64_t M, C;             /* rows, channels: M >= 0, 8 <= C <= 16384, C % 8 == 0         */
-  int32_t n_seg;            /* samples, >= 1                                               */
+  int32_t n_seg;            /* samples, 1 <= n_seg <= 65000                                */
   int32_t stream_dtype;     /* FT_BF16 or FT_F32: x, r, dr, dx.  Everything else is bf16   */
   const int32_t* seg;       /* device [n_seg + 1], ascending: sample b has the rows seg[b] ..
                                seg[b+1] - 1 (it may have none).  Rows before seg[1] belong to
@@ -524,7 +524,7 @@ typedef struct {
   int32_t Hq, Hkv, D;       /* heads of queries and of keys and values; D = 64 or 128      */
   int32_t mask;             /* ft_attn_mask                                                */
   float scale, softcap;     /* scale > 0; softcap >= 0 (0: none)                           */
-  int32_t n_doc;            /* documents, >= 1                                             */
+  int32_t n_doc;            /* documents, >= 1; (M / 64 + n_doc + 2) Hq <= 2^22            */
   const int32_t* doc;       /* device [n_doc + 1], ascending: document d has the rows doc[d]
                                .. doc[d+1] - 1 (it may have none); NULL: one document of
                                all rows (n_doc == 1)                                       */
@@ -598,7 +598,7 @@ typedef struct {
  * fourtune_adamw_plan checks the tensors, fills `host_table` (host memory)
  * and d's n_tensors, has_master, arena and n_chunks.  The caller copies the table to the
  * device, sets d->table, d->m .. d->v_scale, and keeps all of them.
- * arena < 2^32.  Errors: FT_EINVAL, FT_ESHAPE, FT_EALIGN. */
+ * arena < 2^32, at most 2^23 chunks of 2048 elements.  Errors: FT_EINVAL, FT_ESHAPE, FT_EALIGN. */
 size_t fourtune_adamw_plan_bytes(const ft_adamw_tensor* tensors, int32_t n_tensors,
                                  int64_t* arena);
 ft_status fourtune_adamw_plan(const ft_adamw_tensor* tensors, int32_t n_tensors,

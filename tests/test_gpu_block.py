@@ -492,6 +492,24 @@ def test_attention_offsets_past_32_bits():
     assert torch.equal(h[M - 150:], h2)
 
 
+def test_more_rows_than_one_grid_axis():
+    """Row counts past what one axis of a grid of workgroups counts."""
+    norm = block.GatedNorm()
+    x = torch.randn(2_200_003, 8, dtype=F32, device=DEV).to(BF)
+    _, h, _ = norm.forward(x)
+    for a in (0, 2_097_000, 2_198_000):
+        _, part, _ = norm.forward(x[a:a + 2003].contiguous())
+        assert torch.equal(h[a:a + 2003], part)
+    rot = block.AxialRotary(8, [8])
+    M = (1 << 24) + 5
+    pos = (torch.arange(M, dtype=torch.int32, device=DEV) % 1000)[:, None].contiguous()
+    q = x[:, :8].repeat(8, 1)[:M].unflatten(1, (1, 8))
+    a, b = rot.forward(q, q, pos)
+    for s in (slice(0, 100), slice((1 << 23) - 50, (1 << 23) + 50), slice(M - 100, M)):
+        c, d = rot.forward(q[s].contiguous(), q[s].contiguous(), pos[s].contiguous())
+        assert torch.equal(a[s], c) and torch.equal(b[s], d)
+
+
 # ------------------------------------------------------------------ AdamW
 SIZES = (1, 7, 8, 127, 128, 0, 129, 2047, 2048, 2049, 5000)
 HYPER = dict(lr=1e-2, betas=(0.9, 0.99), eps=1e-6, weight_decay=0.1)
@@ -590,7 +608,17 @@ def test_adamw_8bit_states_at_the_ends_of_the_range():
     assert np.isnan(m[6]) and np.isnan(r[6]) and np.isinf(m[7]) and np.isinf(r[7])
 
 
-def test_adamw_random_rounding_keeps_small_steps():
+def test_adamw_random_rounding_keeps_nan():
+    """A NaN of any payload stays one in a parameter that is rounded at random."""
+    bits = torch.tensor([0x7FFFFFFF, 0x7FC00000, -1, 0x7F800001], dtype=torch.int32, device=DEV)
+    g = bits.repeat(64).view(F32)
+    p = torch.ones(g.numel(), dtype=BF, device=DEV)
+    opt = block.AdamW([p], [g], lr=1e-3, betas=(0.9, 0.99), eps=1e-8, weight_decay=0.0, seed=1)
+    opt.step()
+    assert bool(torch.isnan(p).all())
+
+
+def test_adamw_random_rounding_keeps_small_small_steps():
     """A bf16 parameter without a master moves by a step far below its spacing, on average over elements
     and steps; the mean's deviation is that of independent roundings."""
     n, steps, lr = 1 << 16, 16, 1e-4

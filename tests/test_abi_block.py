@@ -128,6 +128,13 @@ def attn_bwd(d, do=A, ldo=256, q=A, k=A, v=A, o=A, lse=A, dq=A, lq=256, dk=A, lk
     return ops.lib().fourtune_attn_bwd(ctypes.byref(d), do, ldo, q, k, v, o, lse, dq, lq, dk, lk, dv, lv, ws, wsb, None)
 
 
+def test_attention_grid_limit():
+    """Documents times heads have to fit one grid of workgroups."""
+    assert attn_fwd(attn(n_doc=(1 << 20) - 3)) == OK and attn_bwd(attn(n_doc=(1 << 20) - 3)) == OK
+    assert attn_fwd(attn(n_doc=(1 << 20) - 2)) == ops.FT_ESHAPE
+    assert attn_bwd(attn(n_doc=(1 << 20) - 2)) == ops.FT_ESHAPE
+
+
 def test_attention_refusals():
     assert attn_fwd(attn()) == OK and attn_bwd(attn()) == OK
     for kw in (dict(M=-1), dict(D=96), dict(D=32), dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(n_doc=0), dict(doc=None),

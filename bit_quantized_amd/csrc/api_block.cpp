@@ -325,7 +325,7 @@ ft_status fourtune_attn_fwd(const ft_attn* d, const uint16_t* q, const uint16_t*
 size_t fourtune_attn_workspace_bytes(const ft_attn* d) {
   if (attn_shape(d) != FT_OK) return 0;
   return align_up(static_cast<size_t>(d->M) * d->Hq * sizeof(float) + 1) +
-         align_up(ft::attn_part_bytes(d->M, d->Hq, d->Hkv, d->D));
+         align_up(ft::attn_part_bytes(d->M, d->Hq, d->Hkv, d->D, ft::attn_uneven(d->mask, d->n_doc)));
 }
 
 ft_status fourtune_attn_bwd(const ft_attn* d, const uint16_t* d_o, int64_t ld_do,

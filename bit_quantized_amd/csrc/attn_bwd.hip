@@ -531,7 +531,7 @@ hipError_t dq_go(const AttnArgs& a, hipStream_t st) {
 template <int D, bool CAP, int NW, int G>
 hipError_t dkv_go(const AttnArgs& a, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>(tiles_of<32 * NW / G>(a));
-  if (!attn_split_heads(a.M, a.Hq, a.Hkv)) {
+  if (!attn_split_heads(a.M, a.Hq, a.Hkv, D, uneven(a))) {
     hipLaunchKernelGGL((k_attn_dkv<D, CAP, NW, G, 32, false>), dim3(tiles * static_cast<uint32_t>(a.Hkv)), dim3(64 * NW),
                        0, st, a, tiles);
     return hipGetLastError();
@@ -567,7 +567,7 @@ hipError_t dkv_go(const AttnArgs& a, hipStream_t st) {
 // of 128: 9.8 us by four groups, 8.0 by two).
 template <int D, bool CAP>
 hipError_t go(const AttnArgs& a, hipStream_t st) {
-  const int64_t heads = attn_split_heads(a.M, a.Hq, a.Hkv) ? a.Hq : a.Hkv;       // of dK and dV
+  const int64_t heads = attn_split_heads(a.M, a.Hq, a.Hkv, D, uneven(a)) ? a.Hq : a.Hkv;       // of dK and dV
   const int64_t t32 = (a.M + 31) / 32, t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
   const int64_t each = a.M / a.n_doc;
   if constexpr (D == 64) {
@@ -593,9 +593,19 @@ hipError_t go(const AttnArgs& a, hipStream_t st) {
 
 }  // namespace
 
-bool attn_split_heads(int64_t M, int Hq, int Hkv) { return Hq > Hkv && M * Hkv < int64_t(512) * 128; }
-size_t attn_part_bytes(int64_t M, int Hq, int Hkv, int D) {
-  return attn_split_heads(M, Hq, Hkv) ? static_cast<size_t>(M) * Hq * 2 * D * sizeof(float) : 0;
+// Whether the query heads of a key head go to workgroups of their own, whose
+// sums a further kernel adds (4 to 5 us), instead of being walked one after
+// the other.  That pays where the walk is long and leaves CUs free, for longer
+// where the workgroups' lengths differ; us, walked / divided:
+//   heads of 64:   12 on 4, 64 rows 6.6 / 8.4; 4 on 1, 256 rows 11.8 / 9.6, 4096 rows 131 / 57;
+//                  12 on 4, 1024 rows 28 / 21, 2048 rows 54 / 54, 4096 rows 145 / 158 (causal 122 / 107)
+//   heads of 128:  16 on 8, 256 rows 13.7 / 13.9, 2048 rows 99 / 85, 4096 rows 279 / 287 (causal 232 / 174)
+bool attn_split_heads(int64_t M, int Hq, int Hkv, int D, bool uneven) {
+  const int64_t most = D == 64 ? (uneven ? 16384 : 8192) : (uneven ? 65536 : 24576);
+  return (Hq / Hkv - 1) * M >= 384 && M * Hkv <= most;
+}
+size_t attn_part_bytes(int64_t M, int Hq, int Hkv, int D, bool uneven) {
+  return attn_split_heads(M, Hq, Hkv, D, uneven) ? static_cast<size_t>(M) * Hq * 2 * D * sizeof(float) : 0;
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st) {

@@ -99,9 +99,7 @@ inline int64_t tiles_of(const AttnArgs& a) {
   return a.doc ? a.M / BM + a.n_doc + 2 : (a.M + BM - 1) / BM;
 }
 
-// Whether the workgroups' lengths differ: under a causal or prefix mask, and
-// among the documents of a packed batch.
-inline bool uneven(const AttnArgs& a) { return a.mask != 0 || a.n_doc > 2; }
+inline bool uneven(const AttnArgs& a) { return attn_uneven(a.mask, a.n_doc); }
 
 // Whether the forward's workgroups of heads of 128 have eight waves (256
 // queries) that take turns, or four (128) that do not.  Eight are faster while most CUs have

@@ -294,8 +294,11 @@ struct AttnArgs {
 };
 // The query heads of a key head are divided between workgroups where whole
 // key heads would be fewer than 512 of them.
-bool attn_split_heads(int64_t M, int Hq, int Hkv);
-size_t attn_part_bytes(int64_t M, int Hq, int Hkv, int D);
+// Whether the workgroups' lengths differ: under a causal or prefix mask, and
+// among the documents of a packed batch.
+inline bool attn_uneven(int mask, int n_doc) { return mask != 0 || n_doc > 2; }
+bool attn_split_heads(int64_t M, int Hq, int Hkv, int D, bool uneven);
+size_t attn_part_bytes(int64_t M, int Hq, int Hkv, int D, bool uneven);
 hipError_t launch_attn_fwd(const AttnArgs& a, int D, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnArgs& a, int D, hipStream_t st);
 
